@@ -232,6 +232,169 @@ sa_status sparse_attn_decode_prior(const sa_params* p, int32_t pos, const void* 
                                    float* lse, void* stream);
 
 /*
+ * ---- Norms of queries and keys ---------------------------------------------
+ * For every row x of q and of k (head dim D), with one weight vector w per layer
+ * and tensor:
+ *   r = 1 / sqrt(mean(x^2) + eps),   y = R(pos) (x r w)
+ * R is the rotation of the forward (rotate-half pairs, angles in double
+ * precision rounded to fp32) at position pos = pos0 + t; rotate = 0 leaves it
+ * out: sparse_attn_fwd and sparse_attn_decode rotate by themselves, the paged
+ * cache and sparse_attn_chunk expect rotated rows (sparse_attn_cache_append does
+ * norm and rotation in its own pass). Without weights (both NULL) there is no
+ * norm, only the rotation. Sums are fp32, one rounding to dtype at the end.
+ * (The paper has no counterpart: query/key norms are the training-stability
+ * option of the models that such an attention serves.)
+ *   q : device rows [L][B][Hq][T][D], k : [L][B][Hkv][T][D], of any strides
+ *       that are multiples of 16 bytes, D innermost and contiguous; base
+ *       pointers 16-byte aligned                                       (read)
+ *   q_weight, k_weight : device fp32 [L][D], 16-byte aligned, or both NULL (read)
+ *   q_out, k_out : contiguous, as q and k; may be q and k themselves where those
+ *       are contiguous, else they must not overlap them             (written)
+ * Backward, for the outputs' gradients dq_out and dk_out (strided like q and k):
+ *   dq, dk : contiguous; may be dq_out and dk_out themselves where those are
+ *       contiguous                                                   (written)
+ *   dq_weight, dk_weight : device fp32 [L][D], summed over batch, heads and rows
+ *       in a fixed order; NULL exactly where the weights are         (written)
+ *   workspace : at least sparse_attn_qk_norm_workspace_size bytes, 16-byte
+ *       aligned; one call's at a time (calls that may overlap, captured graphs
+ *       among them, need one each). 0 bytes without weights.
+ * B = 0 or T = 0 is a call without rows: it writes zero weight gradients.
+ */
+typedef struct {
+  int64_t layer, batch, head, row; /* distances in elements */
+} sa_head_strides;
+
+typedef struct {
+  int32_t L, B, Hq, Hkv, T, D; /* layers, batch, query heads, key heads, rows, head dim */
+  int32_t pos0;                /* position of row 0, >= 0                               */
+  int32_t rotate;              /* 0: no rotation                                        */
+  float eps;                   /* >= 0                                                  */
+  float rope_base;             /* > 0                                                   */
+  sa_dtype dtype;              /* of q, k and everything shaped like them               */
+} sa_qk_norm_params;
+
+size_t sparse_attn_qk_norm_workspace_size(const sa_qk_norm_params* p);
+sa_status sparse_attn_qk_norm_rope(const sa_qk_norm_params* p, const void* q,
+                                   const sa_head_strides* q_strides, const void* k,
+                                   const sa_head_strides* k_strides, const float* q_weight,
+                                   const float* k_weight, void* q_out, void* k_out, void* stream);
+sa_status sparse_attn_qk_norm_rope_bwd(const sa_qk_norm_params* p, const void* q,
+                                       const sa_head_strides* q_strides, const void* k,
+                                       const sa_head_strides* k_strides, const float* q_weight,
+                                       const float* k_weight, const void* dq_out,
+                                       const sa_head_strides* dq_out_strides, const void* dk_out,
+                                       const sa_head_strides* dk_out_strides, void* dq, void* dk,
+                                       float* dq_weight, float* dk_weight, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * ---- Paged key/value cache ---------------------------------------------------
+ * Pages of page_size rows, [L][n_pages][Hkv][page_size][D], contiguous, one
+ * array for keys and one for values. page_table [B][max_pages] (int32, device)
+ * names the pages of every sequence: row r of sequence b lies in slot
+ * r % page_size of page page_table[b][r / page_size], the same page in every
+ * layer. Only entries of rows that a call touches are looked at. Two formats:
+ *   SA_CACHE_PLAIN  rows of params.dtype
+ *   SA_CACHE_E4M3   one byte per element (e4m3: 4 exponent, 3 mantissa bits,
+ *                   largest value 448) and one fp32 scale per row, in k_scale /
+ *                   v_scale [L][n_pages][Hkv][page_size]: value = code * scale.
+ *                   Written rows get scale = 2^max(-100, ceil(log2(amax/448))), a
+ *                   power of two, and codes rounded to nearest even from fp32;
+ *                   a row that holds an infinity or a NaN gets a NaN scale.
+ * Keys are held rotated.
+ *
+ * New tokens of one call: N rows, sequence b's are rows cu_q[b] .. cu_q[b+1]-1
+ * (cu_q: device int32 [B+1], not decreasing, cu_q[0] >= 0), at positions
+ * cached[b], cached[b]+1, ... (cached: device int32 [B], the rows that the
+ * sequence holds before). A sequence may have none. Rows that belong to no
+ * sequence (below cu_q[0], or from cu_q[B] on) are padding: nothing is read for
+ * them and their outputs stay as they were. cu_q, cached and page_table are read
+ * on the device, so a captured graph follows their contents; a page index
+ * outside [0, n_pages), or a position outside [0, max_pages * page_size), sets
+ * bit 3 of the device error word and no such row is touched: appends skip the
+ * row (its query is NaN when the position is out of range), reads and attention
+ * give NaN for what would have depended on it, and may do so for the up to 7
+ * neighbouring tokens of the sequence. No two sequences with new tokens may write
+ * to the same page.
+ *
+ * Limits: D in {16, 32, 64, 128}; max_pages * page_size <= 2^24; n_pages * Hkv *
+ * page_size < 2^31; L and Hq + 2 Hkv at most 65535 (cache_read: B * Hkv). N = 0
+ * and B = 0 are calls without work.
+ */
+typedef enum { SA_CACHE_PLAIN = 0, SA_CACHE_E4M3 = 1 } sa_cache_format;
+
+typedef struct {
+  int64_t layer, row, head; /* distances in elements, multiples of 16 bytes */
+} sa_row_strides;
+
+typedef struct {
+  int32_t L, N, B;       /* layers, rows of new tokens, sequences             */
+  int32_t Hq, Hkv, D;    /* query heads (a multiple of Hkv), key/value heads  */
+  int32_t n_pages, page_size, max_pages;
+  sa_dtype dtype;        /* of q, k, v, o and plain pages                     */
+  sa_cache_format format;
+} sa_paged_params;
+
+typedef struct {
+  void* k;                   /* device, 16-byte aligned                        */
+  void* v;
+  float* k_scale;            /* device, NULL exactly for SA_CACHE_PLAIN        */
+  float* v_scale;
+  const int32_t* page_table; /* device [B][max_pages]                          */
+} sa_pages;
+
+/*
+ * Append: writes the new tokens' rotated keys and their values into the cache,
+ * and returns their rotated queries, in one pass. With weights (fp32 [L][D],
+ * 16-byte aligned, both or neither) queries and keys are normed first, as in
+ * sparse_attn_qk_norm_rope. q, k, v: rows [L][N][heads][D] of any strides that
+ * are multiples of 16 bytes (slices of one projection's output), 16-byte aligned;
+ * q_out: contiguous [L][N][Hq][D], not overlapping them.
+ */
+sa_status sparse_attn_cache_append(const sa_paged_params* p, const sa_pages* pages,
+                                   const int32_t* cu_q, const int32_t* cached, const void* q,
+                                   const sa_row_strides* q_strides, const void* k,
+                                   const sa_row_strides* k_strides, const void* v,
+                                   const sa_row_strides* v_strides, const float* q_weight,
+                                   const float* k_weight, float eps, float rope_base, void* q_out,
+                                   void* stream);
+
+/*
+ * Read back: rows 0 .. lengths[b] - 1 (lengths: device int32 [B]) of every
+ * sequence to contiguous k and v [L][B][Hkv][rows][D] of params.dtype; at most
+ * `rows` of them, and rows from lengths[b] on stay as they were. N and Hq are not
+ * looked at.
+ */
+sa_status sparse_attn_cache_read(const sa_paged_params* p, const sa_pages* pages,
+                                 const int32_t* lengths, int32_t rows, void* k, void* v,
+                                 void* stream);
+
+/*
+ * Attention of the new tokens over the cache, which holds their own rows already
+ * (sparse_attn_cache_append): each token attends what row pos of sparse_attn_fwd
+ * attends (window, sinks, interpolated offsets, one softmax; Hq / Hkv query heads
+ * share a key/value head), whatever the number of new tokens: one per sequence is
+ * a decode step, many are a prefill, and one call may mix them.
+ *   q     : rotated rows [L][N][Hq][D], strides as above               (read)
+ *   alpha : device fp32 [L]                                             (read)
+ *   beta  : device fp32 [L][N][Hq] or NULL: the log-prior of
+ *           sparse_attn_fwd_prior on the offset members                 (read)
+ *   o     : contiguous [L][N][Hq][D] of params.dtype                  (written)
+ *   lse   : device fp32 [L][N][Hq] or NULL                            (written)
+ *   window, n_offsets, offsets (host), n_sinks, scale: as in sa_params; any
+ *           window.
+ * Scores and softmax are fp32; with bf16 queries the probabilities are rounded
+ * to bf16 for their product with the values. Masked rows do not reach a query,
+ * whatever they hold. Source: the attended set, scaling and interpolation of
+ * "Depth-Staggered Fibonacci Spacing for Sparse Attention" (Methodology).
+ */
+sa_status sparse_attn_chunk(const sa_paged_params* p, const sa_pages* pages, const int32_t* cu_q,
+                            const int32_t* cached, const void* q, const sa_row_strides* q_strides,
+                            const float* alpha, const float* beta, int32_t window,
+                            int32_t n_offsets, const int32_t* offsets, int32_t n_sinks,
+                            float scale, void* o, float* lse, void* stream);
+
+/*
  * Learned-alpha parametrisation.  The page trains "one free parameter theta
  * per layer, initialised at alpha = 1" and constrains alpha to [0.5, 1.5]
  * (Methodology: scaling; experimental variables); it does not give the map.
@@ -279,7 +442,7 @@ sa_status sparse_attn_fwd_noalloc(const sa_params* p, const void* q, const void*
                                   void* stream);
 
 /*
- * Device error word of the staged kernels.  Reading synchronises with the
+ * Device error word of the staged and the paged kernels.  Reading synchronises with the
  * device; with clear != 0 the word is reset.  Returns -1 on a CUDA error.
  *   bit 0: a bounded wait for a staging copy gave up (the kernel then left
  *          its outputs incomplete and returned rather than wait without end);
@@ -291,7 +454,10 @@ sa_status sparse_attn_fwd_noalloc(const sa_params* p, const void* q, const void*
  *          |RoPE(K)| / 256 (and, in the backward, |RoPE(Q)| * scale / 256)
  *          above 65504, i.e. rotated key or scaled query elements beyond about
  *          1.68e7; for the tensor-core forward also |RoPE(Q)| * scale above
- *          65504.  Outputs of such a call are not valid.
+ *          65504.  Outputs of such a call are not valid;
+ *   bit 3: a page index or a position of the paged cache outside its range
+ *          (sparse_attn_cache_append / _cache_read / _chunk): no such row was
+ *          touched, and the outputs that depend on it are NaN.
  */
 int32_t sparse_attn_device_error(int clear);
 

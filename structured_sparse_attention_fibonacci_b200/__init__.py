@@ -10,6 +10,9 @@ present, the calls raise.
     O, lse = fwd(q, k, v, alpha, window=12)                 # [L, B, H, T, D]
     dq, dk, dv, dalpha = bwd(q, k, v, O, lse, dO, alpha, window=12)
 
+``paged.py`` binds the query/key norm, the paged cache and the attention over
+it (qk_norm_rope, cache_append, cache_read, chunk_attn).
+
 Method: "Depth-Staggered Fibonacci Spacing for Sparse Attention" (C. A.
 Capps), technical summary, Methodology -- "Attended set", "Scaling",
 "Implementation".
@@ -39,10 +42,13 @@ EXPORTED = ("sparse_attn_fwd", "sparse_attn_bwd", "sparse_attn_workspace_size",
             "sparse_attn_context_size", "sparse_attn_fwd_train", "sparse_attn_bwd_ctx",
             "sparse_attn_decode", "sparse_attn_alpha_from_theta", "sparse_attn_dtheta",
             "sparse_attn_fwd_prior", "sparse_attn_bwd_prior", "sparse_attn_decode_prior",
-            "sparse_attn_set_wait_limit", "sparse_attn_plant_stall", "sparse_attn_diag_fma_probe")
+            "sparse_attn_set_wait_limit", "sparse_attn_plant_stall", "sparse_attn_diag_fma_probe",
+            "sparse_attn_qk_norm_workspace_size", "sparse_attn_qk_norm_rope",
+            "sparse_attn_qk_norm_rope_bwd", "sparse_attn_cache_append", "sparse_attn_cache_read",
+            "sparse_attn_chunk")
 
 # Device error word bits (sparse_attn_device_error)
-ERR_WAIT, ERR_BOUNDS, ERR_RANGE = 1, 2, 4
+ERR_WAIT, ERR_BOUNDS, ERR_RANGE, ERR_PAGE = 1, 2, 4, 8
 
 
 class SaParams(ctypes.Structure):
@@ -126,6 +132,7 @@ def lib():
         L.sparse_attn_trace_read.argtypes = [ctypes.c_int32, ctypes.POINTER(ctypes.c_char_p),
                                              ctypes.POINTER(ctypes.c_double),
                                              ctypes.POINTER(ctypes.c_int32)]
+        _bind_paged(L)
         _lib = L
     return _lib
 
@@ -180,7 +187,8 @@ def select_forward(which: int = 0) -> None:
 def device_error(clear: bool = True) -> int:
     """Device error word of the staged kernels (ERR_WAIT: a bounded staging
     wait gave up; ERR_BOUNDS: a bounds violation seen by the bounds-checking
-    build; ERR_RANGE: an input beyond the staged operands' fp16 range);
+    build; ERR_RANGE: an input beyond the staged operands' fp16 range; ERR_PAGE:
+    a page index or a position of the paged cache outside its range);
     synchronises with the device; cleared after reading by default."""
     return int(lib().sparse_attn_device_error(int(bool(clear))))
 
@@ -461,3 +469,8 @@ def bwd(q, k, v, o, lse, dout, alpha, *, window, offsets=FIB15, sinks=0, rope_ba
                            _ptr(workspace), workspace.numel(), _stream_handle(stream))
     _check("sparse_attn_bwd", st)
     return dq, dk, dv, dalpha
+
+
+from .paged import (PagedCache, cache_append, cache_read, chunk_attn, paged_cache,  # noqa: E402
+                    qk_norm_rope, qk_norm_rope_bwd, qk_norm_workspace_size)
+from .paged import _bind as _bind_paged  # noqa: E402

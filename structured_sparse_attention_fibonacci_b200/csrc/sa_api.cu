@@ -115,6 +115,12 @@ cudaError_t launch_fwd_dispatch(const Problem& pb, const FwdPtrs& a, cudaStream_
              : launch_fwd_general(pb, a, st, launches);
 }
 
+sa_status rope_table_for(int T, int D, float base, cudaStream_t st, const float2** out) {
+  return rope_table(T, D, base, st, out);
+}
+
+void set_last_launches(int n) { g_last_launches = n; }
+
 WaitCfg wait_cfg() { return WaitCfg{g_wait_limit, g_plant_stall}; }
 
 void trace_mark(const char* kernel, cudaStream_t st, bool begin) {
@@ -194,14 +200,16 @@ int32_t sparse_attn_trace_read(int32_t max, const char** names, double* total_ms
 }
 
 int32_t sparse_attn_device_error(int clear) {
-  unsigned fwd = 0, fwd_tc = 0, fwd_umma = 0, bwd = 0, prep = 0;
+  unsigned fwd = 0, fwd_tc = 0, fwd_umma = 0, bwd = 0, prep = 0, cache = 0, chunk = 0;
   if (sa::fast_fwd_read_error(&fwd, clear != 0) != cudaSuccess ||
       sa::fast_fwd_tc_read_error(&fwd_tc, clear != 0) != cudaSuccess ||
       sa::fwd_umma_read_error(&fwd_umma, clear != 0) != cudaSuccess ||
       sa::fast_bwd_read_error(&bwd, clear != 0) != cudaSuccess ||
-      sa::prep_read_error(&prep, clear != 0) != cudaSuccess)
+      sa::prep_read_error(&prep, clear != 0) != cudaSuccess ||
+      sa::cache_read_error(&cache, clear != 0) != cudaSuccess ||
+      sa::chunk_read_error(&chunk, clear != 0) != cudaSuccess)
     return -1;
-  return (int32_t)(fwd | fwd_tc | fwd_umma | bwd | prep);
+  return (int32_t)(fwd | fwd_tc | fwd_umma | bwd | prep | cache | chunk);
 }
 
 size_t sparse_attn_workspace_size(const sa_params* p, int backward) {

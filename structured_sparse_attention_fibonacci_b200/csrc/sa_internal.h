@@ -160,4 +160,70 @@ cudaError_t launch_decode(const Problem& pb, int pos, const void* q, const void*
 cudaError_t launch_fwd_general(const Problem& pb, const FwdPtrs& a, cudaStream_t st, int* launches);
 cudaError_t launch_bwd_general(const Problem& pb, const BwdPtrs& a, cudaStream_t st, int* launches);
 
+// ---- query/key norm, paged cache, chunk attention ----------------------------
+// The RoPE table of positions 0 .. T-1 on the current device (sa_api.cu).
+sa_status rope_table_for(int T, int D, float base, cudaStream_t st, const float2** out);
+// What sparse_attn_last_launch_count reports next (sa_api.cu).
+void set_last_launches(int n);
+
+// Norms of queries and keys (sa_norm.cu).
+struct NormProblem {
+  int L, B, Hq, Hkv, T, D, pos0;
+  bool rotate;
+  float eps;
+  sa_dtype dtype;
+};
+struct NormPtrs {
+  const void* q; const void* k;
+  sa_head_strides qs, ks;
+  const float* q_weight; const float* k_weight;  // both or neither
+  const void* dq_out; const void* dk_out;        // backward: the outputs' gradients
+  sa_head_strides dqs, dks;
+  void* q_dst; void* k_dst;                      // outputs (forward) or dq, dk (backward)
+  const float2* rope;                            // nullptr without the rotation
+};
+size_t qk_norm_workspace(const NormProblem& p);
+cudaError_t launch_qk_norm(const NormProblem& p, const NormPtrs& x, cudaStream_t st);
+cudaError_t launch_qk_norm_bwd(const NormProblem& p, const NormPtrs& x, float* dqw, float* dkw,
+                               void* ws, cudaStream_t st, int* launches);
+
+// Paged cache (sa_cache.cu) and the attention over it (sa_chunk.cu).
+struct PagedProblem {
+  int L, N, B, Hq, Hkv, D, n_pages, page_size, max_pages;
+  sa_dtype dtype;
+  sa_cache_format format;
+};
+struct PagedPtrs {
+  void* k; void* v; float* k_scale; float* v_scale;
+  const int32_t* table;
+};
+struct AppendPtrs {
+  const void* q; const void* k; const void* v;
+  sa_row_strides qs, ks, vs;
+  const float* q_weight; const float* k_weight;  // both or neither
+  float eps;
+  const int32_t* cu_q; const int32_t* cached;
+  const float2* rope;
+  void* q_out;
+};
+struct ChunkPtrs {
+  const void* q;
+  sa_row_strides qs;
+  const int32_t* cu_q; const int32_t* cached;
+  const float* alpha; const float* beta;
+  int W, n_off, S;
+  int f[SA_MAX_OFFSETS];
+  float scale;
+  void* o; float* lse;
+};
+cudaError_t launch_cache_append(const PagedProblem& p, const PagedPtrs& c, const AppendPtrs& x,
+                                cudaStream_t st);
+cudaError_t launch_cache_read(const PagedProblem& p, const PagedPtrs& c, const int* lengths,
+                              int rows, void* k, void* v, cudaStream_t st);
+cudaError_t launch_chunk_attn(const PagedProblem& p, const PagedPtrs& c, const ChunkPtrs& x,
+                              cudaStream_t st);
+// Their device error words (bit 3: a page index or position outside its range).
+cudaError_t cache_read_error(unsigned* out, bool clear);
+cudaError_t chunk_read_error(unsigned* out, bool clear);
+
 }  // namespace sa
