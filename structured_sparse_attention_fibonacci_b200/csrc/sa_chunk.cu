@@ -71,12 +71,33 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// One m16n8k16 product with fp32 sums, of bf16 (plain rows) or fp16 (e4m3 rows,
+// whose codes are exact in fp16) operands.
+template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return pack_bf16x2(lo, hi);
+  }
 }
 
 // Transpose of an 8x8 matrix of 16-bit values (lane (g, c) holds row g, columns
@@ -111,98 +132,98 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
 //              element (8 i + g) VE.
 template <int D, bool E4M3>
 struct Lay {
-  static constexpr int kElt = E4M3 ? 1 : 2;
+  static constexpr int kElt = E4M3 ? 1 : 2, kRow = D * kElt;      // bytes
   static constexpr int kFull = 16 / kElt;
   static constexpr int KE = D / 4 < kFull ? D / 4 : kFull, KP = D / 4 / KE;
   static constexpr int VE = D / 8 < kFull ? D / 8 : kFull, VP = D / 8 / VE;
+  static constexpr int KW = D / 4 * kElt / 4;                     // words of a K part
+  static constexpr int VN = VE * kElt < 4 ? 1 : VE * kElt / 4;    // words of a V piece
 };
 
-// This quad lane's D/4 elements of cache row `row` (row < 0: zeros) as bf16 pairs.
+// Two e4m3 codes as two fp16 values: exact, NaN kept.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t h;
+  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"(two));
+  return h;
+}
+
+// K parts of 16 rows: this lane's of rows g (a) and g + 8 (b) of the tile.
 template <int D, bool E4M3>
-__device__ __forceinline__ void load_k(const uint8_t* base, int row, int c, uint32_t (&w)[D / 8]) {
+struct KTile {
   using Y = Lay<D, E4M3>;
-  if (row < 0) {
+  uint32_t a[Y::KW], b[Y::KW];
+  __device__ __forceinline__ void load(const uint8_t* lane_base, int ra, int rb) {
+    const uint8_t* pa = lane_base + (int64_t)ra * Y::kRow;
+    const uint8_t* pb = lane_base + (int64_t)rb * Y::kRow;
+    constexpr int PB = Y::KE * Y::kElt;      // bytes of a piece
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) w[i] = 0u;
-    return;
-  }
-  const uint8_t* p = base + (size_t)row * (D * Y::kElt) + c * (Y::KE * Y::kElt);
-#pragma unroll
-  for (int i = 0; i < Y::KP; ++i) {
-    if constexpr (E4M3) {
-      constexpr int NW = Y::KE / 4;
-      uint32_t u[NW];
-      load_words<Y::KE>(p + i * 4 * Y::KE, u);
-#pragma unroll
-      for (int j = 0; j < NW; ++j) {
-        w[(i * NW + j) * 2] = e4m3x2_to_bf16x2(u[j] & 0xffffu);
-        w[(i * NW + j) * 2 + 1] = e4m3x2_to_bf16x2(u[j] >> 16);
-      }
-    } else {
-      load_words<Y::KE * 2>(p + i * 8 * Y::KE, w + i * (Y::KE / 2));
+    for (int i = 0; i < Y::KP; ++i) {
+      load_words<PB>(pa + i * 4 * PB, a + i * (PB / 4));
+      load_words<PB>(pb + i * 4 * PB, b + i * (PB / 4));
     }
   }
-}
-
-// S^T of 16 rows (lane's rows: ra = row g, rb = row g + 8) with the 8 columns.
-template <int D, bool E4M3>
-__device__ __forceinline__ void scores(const uint8_t* kb, int ra, int rb, int c,
-                                       const uint32_t (&q)[D / 8], float (&s)[4]) {
-  uint32_t a[D / 8], b[D / 8];
-  load_k<D, E4M3>(kb, ra, c, a);
-  load_k<D, E4M3>(kb, rb, c, b);
-  s[0] = s[1] = s[2] = s[3] = 0.f;
+  // S^T of the 16 rows with the block's 8 columns
+  __device__ __forceinline__ void scores(const uint32_t (&q)[D / 8], float (&s)[4]) const {
+    s[0] = s[1] = s[2] = s[3] = 0.f;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i)
-    mma16816(s, a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1], q[2 * i], q[2 * i + 1]);
-}
+    for (int i = 0; i < D / 16; ++i) {
+      if constexpr (E4M3)
+        mma16816<true>(s, e4m3x2_to_f16x2(a[i] & 0xffffu), e4m3x2_to_f16x2(b[i] & 0xffffu),
+                       e4m3x2_to_f16x2(a[i] >> 16), e4m3x2_to_f16x2(b[i] >> 16), q[2 * i],
+                       q[2 * i + 1]);
+      else
+        mma16816<false>(s, a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1], q[2 * i],
+                        q[2 * i + 1]);
+    }
+  }
+};
 
-// O^T += V^T P^T for 16 rows: this lane's four rows are rows 2c, 2c+1, 2c+8 and
-// 2c+9 of the tile (row < 0: zeros); p0, p1 the fragments of P^T.
+// V parts of 16 rows: this lane's of rows 2c, 2c+1, 2c+8 and 2c+9 of the tile.
 template <int D, bool E4M3>
-__device__ __forceinline__ void values(const uint8_t* vb, const int (&row)[4], int g, uint32_t p0,
-                                       uint32_t p1, float (&o)[D / 16][4]) {
+struct VTile {
   using Y = Lay<D, E4M3>;
-  constexpr int NW = Y::VE * Y::kElt < 4 ? 1 : Y::VE * Y::kElt / 4;      // words of a piece
-  uint32_t u[4][Y::VP * NW];
+  uint32_t u[4][Y::VP * Y::VN];
+  __device__ __forceinline__ void load(const uint8_t* lane_base, int r, int row) {
+    const uint8_t* p = lane_base + (int64_t)row * Y::kRow;
+    constexpr int PB = Y::VE * Y::kElt;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const uint8_t* p = vb + (size_t)max(row[r], 0) * (D * Y::kElt) + g * (Y::VE * Y::kElt);
+    for (int i = 0; i < Y::VP; ++i) load_words<PB>(p + i * 8 * PB, u[r] + i * Y::VN);
+  }
+  // O^T += V^T P^T; p0 and p1: the fragments of P^T
+  __device__ __forceinline__ void add(uint32_t p0, uint32_t p1, float (&o)[D / 16][4]) const {
 #pragma unroll
-    for (int i = 0; i < Y::VP; ++i) {
-      if (row[r] >= 0) {
-        load_words<Y::VE * Y::kElt>(p + i * 8 * Y::VE * Y::kElt, u[r] + i * NW);
+    for (int j = 0; j < D / 16; ++j) {      // head dims 2j and 2j + 1 of this lane's list
+      if constexpr (E4M3) {
+        const int w = j / 2;
+        const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+        const uint32_t x = __byte_perm(u[0][w], u[1][w], sel);
+        const uint32_t y = __byte_perm(u[2][w], u[3][w], sel);
+        mma16816<true>(o[j], e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(x >> 16),
+                       e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(y >> 16), p0, p1);
       } else {
-#pragma unroll
-        for (int j = 0; j < NW; ++j) u[r][i * NW + j] = 0u;
+        mma16816<false>(o[j], __byte_perm(u[0][j], u[1][j], 0x5410),
+                        __byte_perm(u[0][j], u[1][j], 0x7632),
+                        __byte_perm(u[2][j], u[3][j], 0x5410),
+                        __byte_perm(u[2][j], u[3][j], 0x7632), p0, p1);
       }
     }
   }
-#pragma unroll
-  for (int j = 0; j < D / 16; ++j) {      // head dims 2j and 2j + 1 of this lane's list
-    uint32_t a0, a1, a2, a3;
-    if constexpr (E4M3) {
-      const int w = j / 2;
-      const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-      const uint32_t x = __byte_perm(u[0][w], u[1][w], sel), y = __byte_perm(u[2][w], u[3][w], sel);
-      a0 = e4m3x2_to_bf16x2(x & 0xffffu);
-      a1 = e4m3x2_to_bf16x2(x >> 16);
-      a2 = e4m3x2_to_bf16x2(y & 0xffffu);
-      a3 = e4m3x2_to_bf16x2(y >> 16);
-    } else {
-      a0 = __byte_perm(u[0][j], u[1][j], 0x5410);
-      a1 = __byte_perm(u[0][j], u[1][j], 0x7632);
-      a2 = __byte_perm(u[2][j], u[3][j], 0x5410);
-      a3 = __byte_perm(u[2][j], u[3][j], 0x7632);
-    }
-    mma16816(o[j], a0, a1, a2, a3, p0, p1);
-  }
-}
+};
+
+// A lane's walk over the rows that one member has for consecutive tokens: one
+// more row per token, in the same page mostly.
+struct Walk {
+  int row, left;      // pool row of the last token served; rows after it in its page
+};
+
+template <typename QT, int D, bool E4M3>
+__device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, int n, int b,
+                                       int pos, bool inside);
 
 // ---------------------------------------------------------------------------
 // NT: pairs of offset tiles (16 offsets each), 0 .. 2.
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kWarps * 32) k_chunk_tc(const ChunkArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) k_chunk_tc(const __grid_constant__ ChunkArgs a) {
   using Y = Lay<D, E4M3>;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int x = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -243,20 +264,16 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_tc(const ChunkArgs a) {
   }
   const int* table = a.table + (size_t)b * a.max_pages;
   const size_t pool = (size_t)layer * a.n_pages * a.Hkv * a.pd.d;
-  const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.kc) + pool * (D * Y::kElt);
-  const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.vc) + pool * (D * Y::kElt);
+  const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.kc) + pool * Y::kRow + c * Y::KE * Y::kElt;
+  const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.vc) + pool * Y::kRow + g * Y::VE * Y::kElt;
   const float* ks = E4M3 ? a.ks + pool : nullptr;
   const float* vs = E4M3 ? a.vs + pool : nullptr;
   bool lost = !inside;      // a position or page outside its range
   ok = __all_sync(0xffffffffu, ok);
 
-  auto find = [&](int r) {
-    const int row = pool_row(table, a.pd, r, a.n_pages, a.Hkv, h);
-    lost |= row < 0;
-    return row;
-  };
-
-  // query fragments: column g of the block
+  // query fragments: column g of the block. For e4m3 rows in fp16, times a power
+  // of two that brings the column's largest element to [2^14, 2^15): an element
+  // loses bits only where it is 2^28 times smaller.
   uint32_t q[D / 8];
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) q[i] = 0u;
@@ -277,6 +294,23 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_tc(const ChunkArgs a) {
       }
     }
   }
+  float scale[2] = {a.scale * kLog2e, a.scale * kLog2e};      // of the lane's two columns
+  if constexpr (E4M3) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+      top = fmaxf(top, fmaxf(fabsf(bf16lo(q[i])), fabsf(bf16hi(q[i]))));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    int e = (int)(__float_as_uint(top) >> 23) - 127;          // 2^e <= top < 2^(e+1)
+    e = e < -100 || e > 127 ? 14 : e;                         // zeros, infinities: as they are
+    const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+    const float down = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) q[i] = pack16<true>(bf16lo(q[i]) * up, bf16hi(q[i]) * up);
+    scale[0] *= __shfl_sync(0xffffffffu, down, 8 * c);
+    scale[1] *= __shfl_sync(0xffffffffu, down, 8 * c + 4);
+  }
   float beta[2] = {0.f, 0.f};
   if (a.beta) {
 #pragma unroll
@@ -284,251 +318,379 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_tc(const ChunkArgs a) {
       if (tok[e] >= 0)
         beta[e] = kLog2e * __ldg(a.beta + ((size_t)layer * a.N + n0 + tok[e]) * a.Hq + head[e]);
   }
-  const float scale = a.scale * kLog2e;
 
-  // One pass over tokens [ta, tb); more than once only for the tokens of a
-  // block whose outputs are not all finite.
-  int ta = 0, tb = count;
-  bool single = false;
-  while (true) {
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[D / 16][4];
+  // Running reference m and sum l of each of the lane's columns; o the outputs
+  // times l. For e4m3 rows the reference is the maximum of score + log2(value
+  // scale): the weights that go into P V, probability * value scale, are then at
+  // most 1 and fit fp16 whatever the scales.
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[D / 16][4];
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float sig[NT > 0 ? 2 * NT : 1][2];
-    const bool act0 = ok && tok[0] >= ta && tok[0] < tb, act1 = ok && tok[1] >= ta && tok[1] < tb;
+  for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  float sig[NT > 0 ? 2 * NT : 1][2];
 
-    // the lane's offset row in tile pair `pair` for position p: lane c of a quad
-    // finds row a (c even) or b (c odd) of offset g in tile 2 pair + c / 2
-    auto offset_row = [&](int pair, int p) {
-      const int src = pair * 16 + (c >> 1) * 8 + g;
-      const int lo = __shfl_sync(0xffffffffu, off_lo, src);
-      const int cc = __shfl_sync(0xffffffffu, off_c, src);
-      const float w = __shfl_sync(0xffffffffu, off_w, src);
-      const bool there = cc <= p && ((c & 1) == 0 || w != 0.f);
-      return there ? find(p - lo - (c & 1)) : -1;
+  if (ok) {
+    auto find = [&](int r, int& left) {
+      const int lp = quotient(a.pd, r), in = r - lp * a.pd.d;
+      const int page = __ldg(table + lp);
+      left = a.pd.d - 1 - in;
+      if ((unsigned)page >= (unsigned)a.n_pages) {
+        lost = true;
+        left = 0;
+        return 0;
+      }
+      return (page * a.Hkv + h) * a.pd.d + in;
     };
+    auto step_to = [&](Walk& w, int r, int by) {      // from row r - by to row r
+      if (w.left >= by) {
+        w.row += by;
+        w.left -= by;
+      } else {
+        w.row = find(r, w.left);
+      }
+    };
+    // Rows without a member take this row, the first token's own, with weight 0.
+    int unused;
+    const int fill = find(pos0, unused);
+    const bool flat = __all_sync(0xffffffffu, off_w == 0.f);      // integer distances only
 
-    if (ok) {
-      // offset scores
-      if constexpr (NT > 0) {
+    // ---- offset scores -------------------------------------------------------
+    // A tile pair serves 16 offsets. Interpolated: tile i holds, for 8 offsets,
+    // rows a in 0..7 and rows b in 8..15, and lane c of quad g looks up row a (c
+    // even) or b (c odd) of offset g of tile c / 2. Integer distances only: one
+    // tile per token holds 16 offsets; lanes 0..15 look up the rows of token t,
+    // lanes 16..31 those of t + 1.
+    int lo_[NT > 0 ? NT : 1], c_[NT > 0 ? NT : 1];
+    float w_[NT > 0 ? 2 * NT : 1];
+    bool two = true;
 #pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) sig[i][0] = sig[i][1] = -INFINITY;
-        for (int t = ta; t < tb; ++t) {
-          const int p = pos0 + t;
+    for (int pair = 0; pair < NT; ++pair) {
+      const int src = pair * 16 + (flat ? lane & 15 : (c >> 1) * 8 + g);
+      const float w = __shfl_sync(0xffffffffu, off_w, src);
+      lo_[pair] = __shfl_sync(0xffffffffu, off_lo, src) + (flat ? 0 : c & 1);
+      c_[pair] = __shfl_sync(0xffffffffu, off_c, src);
+      if (!flat && (c & 1) && w == 0.f) c_[pair] = 0x7fffffff;      // no second row
+      w_[2 * pair] = __shfl_sync(0xffffffffu, off_w, pair * 16 + g);
+      w_[2 * pair + 1] = __shfl_sync(0xffffffffu, off_w, pair * 16 + 8 + g);
+    }
+    (void)two;
+    const int ahead = flat ? lane >> 4 : 0;       // this lane serves token t + ahead
+    const int stride = flat ? 2 : 1;
+
+    if constexpr (NT > 0) {
 #pragma unroll
-          for (int pair = 0; pair < NT; ++pair) {
-            const int row = offset_row(pair, p);
+      for (int i = 0; i < 2 * NT; ++i) sig[i][0] = sig[i][1] = -INFINITY;
+      Walk w[NT];
+#pragma unroll
+      for (int pair = 0; pair < NT; ++pair) w[pair] = {0, -1};
+      // scores of a tile, times its rows' scales; ra, rb < 0: no member
+      auto tile_scores = [&](const KTile<D, E4M3>& k, int ra, int rb, float (&s)[4]) {
+        k.scores(q, s);
+        if constexpr (E4M3) {
+          const float ka = __ldg(ks + (ra ^ (ra >> 31))), kc = __ldg(ks + (rb ^ (rb >> 31)));
+          s[0] *= ka; s[1] *= ka; s[2] *= kc; s[3] *= kc;
+        }
+      };
+      auto log_scale = [&](int r) {
+        return __log2f(fmaxf(fabsf(__ldg(vs + (r ^ (r >> 31)))), 7.9e-31f));
+      };
+      for (int t = 0; t < count; t += stride) {
+#pragma unroll
+        for (int pair = 0; pair < NT; ++pair) {
+          const int p = pos0 + t + ahead;
+          int row = ~fill;
+          if (c_[pair] <= p && t + ahead < count) {
+            step_to(w[pair], p - lo_[pair], stride);
+            row = w[pair].row;
+          }
+          if (flat) {
+            // tiles of tokens t and t + 1
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int tile = 2 * pair + i;
-              if (i == 1 && tile * 8 >= a.n_off) continue;
+              if (t + i >= count) continue;
+              const int ra = __shfl_sync(0xffffffffu, row, i * 16 + g);
+              const int rb = __shfl_sync(0xffffffffu, row, i * 16 + 8 + g);
+              KTile<D, E4M3> k;
+              k.load(kb, ra ^ (ra >> 31), rb ^ (rb >> 31));
+              float s[4];
+              tile_scores(k, ra, rb, s);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (tok[e] == t + i) {
+                  if (ra >= 0) sig[2 * pair][e] = fmaf(s[e], scale[e], beta[e]);
+                  if (rb >= 0) sig[2 * pair + 1][e] = fmaf(s[2 + e], scale[e], beta[e]);
+                }
+              }
+              if constexpr (E4M3) {
+                const float va = log_scale(ra), vc = log_scale(rb);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (tok[e] == t + i)
+                    m[e] = fmaxf(m[e], fmaxf(sig[2 * pair][e] + va, sig[2 * pair + 1][e] + vc));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (i == 1 && pair * 16 + 8 >= a.n_off) continue;
               const int ra = __shfl_sync(0xffffffffu, row, (lane & 28) + 2 * i);
               const int rb = __shfl_sync(0xffffffffu, row, (lane & 28) + 2 * i + 1);
-              const float w = __shfl_sync(0xffffffffu, off_w, tile * 8 + g);
+              KTile<D, E4M3> k;
+              k.load(kb, ra ^ (ra >> 31), rb ^ (rb >> 31));
               float s[4];
-              scores<D, E4M3>(kb, ra, rb, c, q, s);
-              if constexpr (E4M3) {
-                const float ka = ra >= 0 ? __ldg(ks + ra) : 0.f;
-                const float kb2 = rb >= 0 ? __ldg(ks + rb) : 0.f;
-                s[0] *= ka; s[1] *= ka; s[2] *= kb2; s[3] *= kb2;
+              tile_scores(k, ra, rb, s);
+              const float wb = w_[2 * pair + i], wa = 1.f - wb;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float y = rb >= 0 ? wa * s[e] + wb * s[2 + e] : s[e];
+                if (ra >= 0 && tok[e] == t) sig[2 * pair + i][e] = fmaf(y, scale[e], beta[e]);
               }
-              if (ra >= 0) {
-                const float wa = 1.f - w;
-                const float x0 = w != 0.f ? wa * s[0] + w * s[2] : s[0];
-                const float x1 = w != 0.f ? wa * s[1] + w * s[3] : s[1];
-                if (tok[0] == t) sig[tile][0] = fmaf(x0, scale, beta[0]);
-                if (tok[1] == t) sig[tile][1] = fmaf(x1, scale, beta[1]);
+              if constexpr (E4M3) {
+                float va = log_scale(ra);
+                if (rb >= 0) va = fmaxf(va, log_scale(rb));
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (tok[e] == t) m[e] = fmaxf(m[e], sig[2 * pair + i][e] + va);
               }
             }
           }
         }
+      }
+      if constexpr (!E4M3) {
 #pragma unroll
         for (int i = 0; i < 2 * NT; ++i) {
           m[0] = fmaxf(m[0], sig[i][0]);
           m[1] = fmaxf(m[1], sig[i][1]);
         }
+      }
 #pragma unroll
-        for (int d = 4; d <= 16; d <<= 1) {
-          m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], d));
-          m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], d));
+      for (int d = 4; d <= 16; d <<= 1) {
+        m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], d));
+        m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], d));
+      }
+    }
+
+    // ---- sinks (tile -1) and window, two tiles of 16 rows at a time -------------
+    const int last = pos0 + count - 1;
+    const int base = max(0, pos0 - (a.W - 1));
+    const int tiles = (last - base) / 16 + 1;
+    for (int t0 = a.S > 0 ? -1 : 0; t0 < tiles; t0 += 2) {
+      const int mine = t0 + (lane >> 4);      // the tile this lane looks a row up for
+      const int r_ = mine < 0 ? lane & 15 : base + mine * 16 + (lane & 15);
+      const bool in = r_ <= last && (mine < 0 ? r_ < a.S : mine < tiles);
+      const int row = in ? find(r_, unused) : fill;
+      const bool second = t0 + 1 < tiles;
+      float s[2][4], lv[2][2];
+      int rk[2][2];
+      KTile<D, E4M3> k[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        rk[i][0] = __shfl_sync(0xffffffffu, row, i * 16 + g);
+        rk[i][1] = __shfl_sync(0xffffffffu, row, i * 16 + 8 + g);
+        if (i == 0 || second) k[i].load(kb, rk[i][0], rk[i][1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (i == 1 && !second) {
+          s[1][0] = s[1][1] = s[1][2] = s[1][3] = -INFINITY;
+          continue;
+        }
+        k[i].scores(q, s[i]);
+        const int t = t0 + i;
+        float ka[2] = {scale[0], scale[1]}, kc[2] = {scale[0], scale[1]};
+        if constexpr (E4M3) {
+          const float x0 = __ldg(ks + rk[i][0]), x1 = __ldg(ks + rk[i][1]);
+          ka[0] *= x0; ka[1] *= x0; kc[0] *= x1; kc[1] *= x1;
+        }
+        // lags of rows r and r + 8 from the two columns' positions; sinks have no
+        // far edge but a last row
+        const int r = t < 0 ? g : base + t * 16 + g;
+        const unsigned far = t < 0 ? 0x7fffffffu : (unsigned)a.W;
+        const bool ea = t >= 0 || r < a.S, eb = t >= 0 || r + 8 < a.S;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int lag = pos0 + tok[e] - r;
+          const bool on = tok[e] >= 0;
+          s[i][e] = on && ea && (unsigned)lag < far ? s[i][e] * ka[e] : -INFINITY;
+          s[i][2 + e] = on && eb && (unsigned)(lag - 8) < far ? s[i][2 + e] * kc[e] : -INFINITY;
+        }
+        if constexpr (E4M3) {
+          lv[i][0] = __ldg(vs + rk[i][0]);
+          lv[i][1] = __ldg(vs + rk[i][1]);
         }
       }
-
-      // sinks (tile -1) and window, two tiles of 16 rows at a time
-      const int last = pos0 + tb - 1;
-      const int base = max(0, pos0 + ta - (a.W - 1));
-      const int tiles = (last - base) / 16 + 1;
-      for (int t0 = a.S > 0 ? -1 : 0; t0 < tiles; t0 += 2) {
-        int row[2];
-        float s[2][4];
+      float nm[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = t0 + i;
-          const int r = (t < 0 ? 0 : base + t * 16) + (lane & 15);
-          const bool in = t < 0 ? (r < a.S && r <= last) : (t < tiles && r <= last);
-          row[i] = in ? find(r) : -1;
-        }
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (E4M3) {
+          nm[e] = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = t0 + i;
-          const int ra = __shfl_sync(0xffffffffu, row[i], g);
-          const int rb = __shfl_sync(0xffffffffu, row[i], g + 8);
-          scores<D, E4M3>(kb, ra, rb, c, q, s[i]);
-          float ka = scale, kc = scale;
-          if constexpr (E4M3) {
-            ka = ra >= 0 ? scale * __ldg(ks + ra) : 0.f;
-            kc = rb >= 0 ? scale * __ldg(ks + rb) : 0.f;
-          }
-          const int r = (t < 0 ? 0 : base + t * 16) + g;
-          const int far = t < 0 ? 0x7fffffff : a.W;      // sinks have no lower edge
-          const int p0 = pos0 + tok[0], p1 = pos0 + tok[1];
-          s[i][0] = act0 && ra >= 0 && r <= p0 && p0 - r < far ? s[i][0] * ka : -INFINITY;
-          s[i][1] = act1 && ra >= 0 && r <= p1 && p1 - r < far ? s[i][1] * ka : -INFINITY;
-          s[i][2] = act0 && rb >= 0 && r + 8 <= p0 && p0 - r - 8 < far ? s[i][2] * kc : -INFINITY;
-          s[i][3] = act1 && rb >= 0 && r + 8 <= p1 && p1 - r - 8 < far ? s[i][3] * kc : -INFINITY;
-        }
-        float n0m = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
-        float n1m = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
-#pragma unroll
-        for (int d = 4; d <= 16; d <<= 1) {
-          n0m = fmaxf(n0m, __shfl_xor_sync(0xffffffffu, n0m, d));
-          n1m = fmaxf(n1m, __shfl_xor_sync(0xffffffffu, n1m, d));
-        }
-        n0m = fmaxf(m[0], n0m);
-        n1m = fmaxf(m[1], n1m);
-        const float z0 = n0m == -INFINITY ? 0.f : n0m, z1 = n1m == -INFINITY ? 0.f : n1m;
-        const float f0 = exp2_approx(m[0] - z0), f1 = exp2_approx(m[1] - z1);
-        m[0] = n0m;
-        m[1] = n1m;
-        l[0] *= f0;
-        l[1] *= f1;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          o[j][0] *= f0; o[j][2] *= f0;
-          o[j][1] *= f1; o[j][3] *= f1;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (t0 + i >= tiles) continue;      // uniform
-          float p[4] = {exp2_approx(s[i][0] - z0), exp2_approx(s[i][1] - z1),
-                        exp2_approx(s[i][2] - z0), exp2_approx(s[i][3] - z1)};
-          l[0] += p[0] + p[2];
-          l[1] += p[1] + p[3];
-          if constexpr (E4M3) {
-            const int ra = __shfl_sync(0xffffffffu, row[i], g);
-            const int rb = __shfl_sync(0xffffffffu, row[i], g + 8);
-            const float va = ra >= 0 ? __ldg(vs + ra) : 0.f, vc = rb >= 0 ? __ldg(vs + rb) : 0.f;
-            p[0] = p[0] == 0.f ? 0.f : p[0] * va;
-            p[1] = p[1] == 0.f ? 0.f : p[1] * va;
-            p[2] = p[2] == 0.f ? 0.f : p[2] * vc;
-            p[3] = p[3] == 0.f ? 0.f : p[3] * vc;
-          }
-          const uint32_t p0 = transpose8(pack_bf16x2(p[0], p[1]));
-          const uint32_t p1 = transpose8(pack_bf16x2(p[2], p[3]));
-          const int rows[4] = {__shfl_sync(0xffffffffu, row[i], 2 * c),
-                               __shfl_sync(0xffffffffu, row[i], 2 * c + 1),
-                               __shfl_sync(0xffffffffu, row[i], 2 * c + 8),
-                               __shfl_sync(0xffffffffu, row[i], 2 * c + 9)};
-          values<D, E4M3>(vb, rows, g, p0, p1, o);
-        }
-      }
-
-      // offset values
-      if constexpr (NT > 0) {
-        const float z0 = m[0] == -INFINITY ? 0.f : m[0], z1 = m[1] == -INFINITY ? 0.f : m[1];
-#pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) {
-          sig[i][0] = exp2_approx(sig[i][0] - z0);
-          sig[i][1] = exp2_approx(sig[i][1] - z1);
-          l[0] += sig[i][0];
-          l[1] += sig[i][1];
-        }
-        for (int t = ta; t < tb; ++t) {
-          const int p = pos0 + t;
-#pragma unroll
-          for (int pair = 0; pair < NT; ++pair) {
-            const int row = offset_row(pair, p);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int tile = 2 * pair + i;
-              if (i == 1 && tile * 8 >= a.n_off) continue;
-              const float w = __shfl_sync(0xffffffffu, off_w, tile * 8 + g);
-              float wa = 1.f - w, wb = w;
-              if constexpr (E4M3) {
-                const int ra = __shfl_sync(0xffffffffu, row, (lane & 28) + 2 * i);
-                const int rb = __shfl_sync(0xffffffffu, row, (lane & 28) + 2 * i + 1);
-                wa *= ra >= 0 ? __ldg(vs + ra) : 0.f;
-                wb = rb >= 0 ? wb * __ldg(vs + rb) : 0.f;
-              }
-              const bool on0 = tok[0] == t, on1 = tok[1] == t;
-              const uint32_t p0 = transpose8(pack_bf16x2(on0 ? sig[tile][0] * wa : 0.f,
-                                                         on1 ? sig[tile][1] * wa : 0.f));
-              const uint32_t p1 = transpose8(pack_bf16x2(on0 ? sig[tile][0] * wb : 0.f,
-                                                         on1 ? sig[tile][1] * wb : 0.f));
-              const int rows[4] = {__shfl_sync(0xffffffffu, row, 8 * c + 2 * i),
-                                   __shfl_sync(0xffffffffu, row, 8 * c + 4 + 2 * i),
-                                   __shfl_sync(0xffffffffu, row, 8 * c + 2 * i + 1),
-                                   __shfl_sync(0xffffffffu, row, 8 * c + 4 + 2 * i + 1)};
-              values<D, E4M3>(vb, rows, g, p0, p1, o);
+          for (int i = 0; i < 2; ++i)
+            if (i == 0 || second) {
+              nm[e] = fmaxf(nm[e], s[i][e] + __log2f(fmaxf(fabsf(lv[i][0]), 7.9e-31f)));
+              nm[e] = fmaxf(nm[e], s[i][2 + e] + __log2f(fmaxf(fabsf(lv[i][1]), 7.9e-31f)));
             }
+        } else {
+          nm[e] = fmaxf(fmaxf(s[0][e], s[0][2 + e]), fmaxf(s[1][e], s[1][2 + e]));
+        }
+      }
+#pragma unroll
+      for (int d = 4; d <= 16; d <<= 1) {
+        nm[0] = fmaxf(nm[0], __shfl_xor_sync(0xffffffffu, nm[0], d));
+        nm[1] = fmaxf(nm[1], __shfl_xor_sync(0xffffffffu, nm[1], d));
+      }
+      if (__any_sync(0xffffffffu, nm[0] > m[0] || nm[1] > m[1])) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          nm[e] = fmaxf(nm[e], m[e]);
+          const float f = exp2_approx(m[e] - (nm[e] == -INFINITY ? 0.f : nm[e]));
+          m[e] = nm[e];
+          l[e] *= f;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            o[j][e] *= f;
+            o[j][2 + e] *= f;
+          }
+        }
+      }
+      const float z0 = m[0] == -INFINITY ? 0.f : m[0], z1 = m[1] == -INFINITY ? 0.f : m[1];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (i == 1 && !second) continue;
+        VTile<D, E4M3> v;
+        v.load(vb, 0, __shfl_sync(0xffffffffu, row, i * 16 + 2 * c));
+        v.load(vb, 1, __shfl_sync(0xffffffffu, row, i * 16 + 2 * c + 1));
+        v.load(vb, 2, __shfl_sync(0xffffffffu, row, i * 16 + 2 * c + 8));
+        v.load(vb, 3, __shfl_sync(0xffffffffu, row, i * 16 + 2 * c + 9));
+        float p[4] = {exp2_approx(s[i][0] - z0), exp2_approx(s[i][1] - z1),
+                      exp2_approx(s[i][2] - z0), exp2_approx(s[i][3] - z1)};
+        l[0] += p[0] + p[2];
+        l[1] += p[1] + p[3];
+        if constexpr (E4M3) {
+          p[0] = s[i][0] == -INFINITY ? 0.f : p[0] * lv[i][0];
+          p[1] = s[i][1] == -INFINITY ? 0.f : p[1] * lv[i][0];
+          p[2] = s[i][2] == -INFINITY ? 0.f : p[2] * lv[i][1];
+          p[3] = s[i][3] == -INFINITY ? 0.f : p[3] * lv[i][1];
+        }
+        v.add(transpose8(pack16<E4M3>(p[0], p[1])), transpose8(pack16<E4M3>(p[2], p[3])), o);
+      }
+    }
+
+    // ---- offset values -----------------------------------------------------------
+    if constexpr (NT > 0) {
+      const float z0 = m[0] == -INFINITY ? 0.f : m[0], z1 = m[1] == -INFINITY ? 0.f : m[1];
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) {
+        sig[i][0] = exp2_approx(sig[i][0] - z0);
+        sig[i][1] = exp2_approx(sig[i][1] - z1);
+        l[0] += sig[i][0];
+        l[1] += sig[i][1];
+      }
+      Walk w[NT];
+#pragma unroll
+      for (int pair = 0; pair < NT; ++pair) w[pair] = {0, -1};
+      for (int t = 0; t < count; t += stride) {
+#pragma unroll
+        for (int pair = 0; pair < NT; ++pair) {
+          const int p = pos0 + t + ahead;
+          int row = fill;
+          if (c_[pair] <= p && t + ahead < count) {
+            step_to(w[pair], p - lo_[pair], stride);
+            row = w[pair].row;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // interpolated: tile i of the pair; flat: the tile of token t + i
+            if (flat ? t + i >= count : (i == 1 && pair * 16 + 8 >= a.n_off)) continue;
+            const int s0 = flat ? i * 16 + 2 * c : 8 * c + 2 * i;
+            const int dn = flat ? 1 : 4, db = flat ? 8 : 1;      // next row; row + 8
+            VTile<D, E4M3> v;
+            v.load(vb, 0, __shfl_sync(0xffffffffu, row, s0));
+            v.load(vb, 1, __shfl_sync(0xffffffffu, row, s0 + dn));
+            v.load(vb, 2, __shfl_sync(0xffffffffu, row, s0 + db));
+            v.load(vb, 3, __shfl_sync(0xffffffffu, row, s0 + dn + db));
+            const int at = flat ? t + i : t;
+            const bool on0 = tok[0] == at, on1 = tok[1] == at;
+            float pa0, pa1, pb0, pb1;
+            if (flat) {
+              pa0 = sig[2 * pair][0]; pa1 = sig[2 * pair][1];
+              pb0 = sig[2 * pair + 1][0]; pb1 = sig[2 * pair + 1][1];
+            } else {
+              const float wb = w_[2 * pair + i], wa = 1.f - wb;
+              pa0 = sig[2 * pair + i][0]; pa1 = sig[2 * pair + i][1];
+              pb0 = pa0 * wb; pb1 = pa1 * wb;
+              pa0 *= wa; pa1 *= wa;
+            }
+            if constexpr (E4M3) {
+              const float va = __ldg(vs + __shfl_sync(0xffffffffu, row,
+                                                      flat ? i * 16 + g : (lane & 28) + 2 * i));
+              const float vc = __ldg(vs + __shfl_sync(0xffffffffu, row,
+                                                      flat ? i * 16 + 8 + g
+                                                           : (lane & 28) + 2 * i + 1));
+              pa0 = pa0 == 0.f ? 0.f : pa0 * va;
+              pa1 = pa1 == 0.f ? 0.f : pa1 * va;
+              pb0 = pb0 == 0.f ? 0.f : pb0 * vc;
+              pb1 = pb1 == 0.f ? 0.f : pb1 * vc;
+            }
+            v.add(transpose8(pack16<E4M3>(on0 ? pa0 : 0.f, on1 ? pa1 : 0.f)),
+                  transpose8(pack16<E4M3>(on0 ? pb0 : 0.f, on1 ? pb1 : 0.f)), o);
           }
         }
       }
     }
+  }
 #pragma unroll
-    for (int d = 4; d <= 16; d <<= 1) {
-      l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
-      l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
-    }
-    const bool nan = __any_sync(0xffffffffu, lost) || !ok;
+  for (int d = 4; d <= 16; d <<= 1) {
+    l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
+    l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
+  }
+  const bool nan = __any_sync(0xffffffffu, lost) || !ok;
 
-    if (!single && count > 1 && !nan) {
-      // x - x is 0 for finite x only
-      float z = 0.f;
+  // A weight of 0 does not hide an infinity or a NaN: when an output is not
+  // finite, the block's queries are computed again from their own members alone.
+  float odd = 0.f;      // x - x is 0 for finite x only
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        if (tok[0] >= 0) z += (o[j][0] - o[j][0]) + (o[j][2] - o[j][2]);
-        if (tok[1] >= 0) z += (o[j][1] - o[j][1]) + (o[j][3] - o[j][3]);
-      }
-      if (__any_sync(0xffffffffu, z != 0.f)) {
-        single = true;
-        tb = 1;
-        continue;
-      }
+  for (int j = 0; j < D / 16; ++j) {
+    if (tok[0] >= 0) odd += (o[j][0] - o[j][0]) + (o[j][2] - o[j][2]);
+    if (tok[1] >= 0) odd += (o[j][1] - o[j][1]) + (o[j][3] - o[j][3]);
+  }
+  if (!nan && __any_sync(0xffffffffu, odd != 0.f)) {
+    for (int col = 0; col < count * a.per; ++col) {
+      const int t = col / a.per, hh = col - t * a.per;
+      if (hh < heads)
+        one_query<__nv_bfloat16, D, E4M3>(a, layer, h * a.G + grp * a.per + hh, n0 + t, b,
+                                          pos0 + t, true);
     }
+    return;
+  }
 
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (tok[e] < ta || tok[e] >= tb || tok[e] < 0) continue;
-      const size_t at = ((size_t)layer * a.N + n0 + tok[e]) * a.Hq + head[e];
-      const float bad = __int_as_float(0x7fc00000);
-      const float inv = nan ? bad : 1.f / l[e];
-      __nv_bfloat16* op = reinterpret_cast<__nv_bfloat16*>(a.o) + at * D;
+  for (int e = 0; e < 2; ++e) {
+    if (tok[e] < 0) continue;
+    const size_t at = ((size_t)layer * a.N + n0 + tok[e]) * a.Hq + head[e];
+    const float bad = __int_as_float(0x7fc00000);
+    const float inv = nan ? bad : 1.f / l[e];
+    __nv_bfloat16* op = reinterpret_cast<__nv_bfloat16*>(a.o) + at * D;
 #pragma unroll
-      for (int i = 0; i < Y::VP; ++i) {
-        float x[Y::VE];
+    for (int i = 0; i < Y::VP; ++i) {
+      float y[Y::VE];
 #pragma unroll
-        for (int j = 0; j < Y::VE / 2; ++j) {
-          x[2 * j] = o[i * (Y::VE / 2) + j][e] * inv;
-          x[2 * j + 1] = o[i * (Y::VE / 2) + j][2 + e] * inv;
-        }
-        store_row<__nv_bfloat16, Y::VE>(op + (8 * i + g) * Y::VE, x);
+      for (int j = 0; j < Y::VE / 2; ++j) {
+        y[2 * j] = o[i * (Y::VE / 2) + j][e] * inv;
+        y[2 * j + 1] = o[i * (Y::VE / 2) + j][2 + e] * inv;
       }
-      if (g == 0 && a.lse) a.lse[at] = nan ? bad : kLn2 * (m[e] + log2f(l[e]));
+      store_row<__nv_bfloat16, Y::VE>(op + (8 * i + g) * Y::VE, y);
     }
-    if (!single || tb >= count) break;
-    ta = tb;
-    ++tb;
+    if (g == 0 && a.lse) a.lse[at] = nan ? bad : kLn2 * (m[e] + log2f(l[e]));
   }
   if (__any_sync(0xffffffffu, lost) && lane == 0) atomicOr(&g_chunk_err, kErrPage);
 }
 
 // ---------------------------------------------------------------------------
-// 32-bit queries.
+// 32-bit queries, and the queries that meet infinities or NaN.
 
 // NE consecutive elements of a cache row from element e0, as stored.
-template <bool E4M3, int NE>
+template <bool E4M3, bool BF16, int NE>
 __device__ __forceinline__ void load_part(const uint8_t* base, int D, int row, int e0,
                                           float (&x)[NE]) {
   if constexpr (E4M3) {
@@ -548,6 +710,9 @@ __device__ __forceinline__ void load_part(const uint8_t* base, int D, int row, i
                            x[i * STEP + 2 * j + 1]);
       }
     }
+  } else if constexpr (BF16) {
+    load_row<__nv_bfloat16, NE>(reinterpret_cast<const __nv_bfloat16*>(base) + (size_t)row * D + e0,
+                                x);
   } else {
     const float* p = reinterpret_cast<const float*>(base) + (size_t)row * D + e0;
     if constexpr (NE == 1)
@@ -560,21 +725,17 @@ __device__ __forceinline__ void load_part(const uint8_t* base, int D, int row, i
   }
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const ChunkArgs a) {
+// One query (token row n of sequence b at position pos, query head hq) by one
+// warp: members 32 at a time, and no row but its members' is touched.
+template <typename QT, int D, bool E4M3>
+__device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, int n, int b,
+                                       int pos, bool inside) {
+  constexpr bool BF16 = !E4M3 && sizeof(QT) == 2;
   constexpr int QE = D / 4;                        // elements of a row per quad lane
   constexpr int VE = D >= 32 ? D / 32 : 1;         // value elements per lane
   constexpr int SPLIT = D >= 32 ? 1 : 2;           // D = 16: two members at a time
   const int lane = threadIdx.x & 31, part = lane & 3, mm = lane >> 2;
-  const int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (n >= a.N) return;
-  const int hq = blockIdx.y, h = hq / a.G, layer = blockIdx.z;
-  const int b = find_sequence(a.cu, a.B, 0, n);
-  const int first = __ldg(a.cu + b);
-  if (first < 0 || n < first || n >= __ldg(a.cu + b + 1)) return;
-  const long long posl = (long long)__ldg(a.cached + b) + (n - first);
-  const bool inside = posl >= 0 && posl < (long long)a.max_pages * a.pd.d;
-  const int pos = inside ? (int)posl : 0;
+  const int h = hq / a.G;
 
   int off_lo = 0, off_c = 0x7fffffff;
   float off_w = 0.f;
@@ -588,12 +749,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const ChunkArgs a) {
   bool lost = !inside;
   const int* table = a.table + (size_t)b * a.max_pages;
   const size_t pool = (size_t)layer * a.n_pages * a.Hkv * a.pd.d;
-  const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.kc) + pool * D * (E4M3 ? 1 : 4);
-  const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.vc) + pool * D * (E4M3 ? 1 : 4);
+  constexpr int kElt = E4M3 ? 1 : (int)sizeof(QT);
+  const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.kc) + pool * D * kElt;
+  const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.vc) + pool * D * kElt;
 
   float q[QE];
-  load_row<float, QE>(reinterpret_cast<const float*>(a.q) + layer * a.ql + n * a.qn + hq * a.qh +
-                          part * QE, q);
+  load_row<QT, QE>(reinterpret_cast<const QT*>(a.q) + layer * a.ql + n * a.qn + hq * a.qh +
+                       part * QE, q);
   const size_t at = ((size_t)layer * a.N + n) * a.Hq + hq;
   const float beta = a.beta ? __ldg(a.beta + at) : 0.f;
   const int nw = min(a.W, pos + 1), ns = min(a.S, pos + 1);
@@ -641,7 +803,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const ChunkArgs a) {
       float dot = 0.f;
       if (ia >= 0) {
         float x[QE];
-        load_part<E4M3, QE>(kb, D, ia, part * QE, x);
+        load_part<E4M3, BF16, QE>(kb, D, ia, part * QE, x);
         float t = 0.f;
 #pragma unroll
         for (int e = 0; e < QE; ++e) t = fmaf(q[e], x[e], t);
@@ -649,7 +811,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const ChunkArgs a) {
       }
       if (ib >= 0) {
         float x[QE];
-        load_part<E4M3, QE>(kb, D, ib, part * QE, x);
+        load_part<E4M3, BF16, QE>(kb, D, ib, part * QE, x);
         float t = 0.f;
 #pragma unroll
         for (int e = 0; e < QE; ++e) t = fmaf(q[e], x[e], t);
@@ -682,13 +844,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const ChunkArgs a) {
       const float xb = __shfl_sync(0xffffffffu, vc, src & 31);
       if (ia >= 0) {
         float x[VE];
-        load_part<E4M3, VE>(vb, D, ia, d0, x);
+        load_part<E4M3, BF16, VE>(vb, D, ia, d0, x);
 #pragma unroll
         for (int e = 0; e < VE; ++e) o[e] = fmaf(xa, x[e], o[e]);
       }
       if (ib >= 0) {
         float x[VE];
-        load_part<E4M3, VE>(vb, D, ib, d0, x);
+        load_part<E4M3, BF16, VE>(vb, D, ib, d0, x);
 #pragma unroll
         for (int e = 0; e < VE; ++e) o[e] = fmaf(xb, x[e], o[e]);
       }
@@ -700,15 +862,25 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const ChunkArgs a) {
   const bool nan = __any_sync(0xffffffffu, lost) || !ok;
   const float bad = __int_as_float(0x7fc00000);
   const float inv = nan ? bad : 1.f / l;
-  float* op = reinterpret_cast<float*>(a.o) + at * D + d0;
   if (D >= 32 || lane < 16) {
 #pragma unroll
     for (int e = 0; e < VE; ++e) o[e] *= inv;
-    store_row<float, VE>(reinterpret_cast<float*>(op), o);
+    store_row<QT, VE>(reinterpret_cast<QT*>(a.o) + at * D + d0, o);
   }
   if (lane == 0 && a.lse) a.lse[at] = nan ? bad : kLn2 * m + logf(l);
-  if (lane == 0 && __builtin_expect(!inside, 0)) atomicOr(&g_chunk_err, kErrPage);
-  if (lost && inside) atomicOr(&g_chunk_err, kErrPage);
+  if (lost) atomicOr(&g_chunk_err, kErrPage);
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const __grid_constant__ ChunkArgs a) {
+  const int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (n >= a.N) return;
+  const int b = find_sequence(a.cu, a.B, 0, n);
+  const int first = __ldg(a.cu + b);
+  if (first < 0 || n < first || n >= __ldg(a.cu + b + 1)) return;
+  const long long posl = (long long)__ldg(a.cached + b) + (n - first);
+  const bool inside = posl >= 0 && posl < (long long)a.max_pages * a.pd.d;
+  one_query<float, D, E4M3>(a, blockIdx.z, blockIdx.y, n, b, inside ? (int)posl : 0, inside);
 }
 
 template <int D, bool E4M3>
