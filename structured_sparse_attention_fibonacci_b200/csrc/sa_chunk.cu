@@ -40,6 +40,8 @@
 // 32-bit queries (k_chunk_f32): one warp per (token, query head) on the CUDA
 // cores, chunks of 32 members: four lanes per member for the scores, lanes over
 // head dims for the values.
+#include <type_traits>
+
 #include "sa_paged.cuh"
 
 namespace sa {
@@ -49,12 +51,19 @@ namespace {
 __device__ unsigned g_chunk_err;
 
 constexpr int kWarps = 4;
+#ifndef MB128
+#define MB128 4
+#endif
+#ifndef MB64
+#define MB64 4
+#endif
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct ChunkArgs {
   int L, N, B, Hq, Hkv, n_pages, max_pages, W, n_off, S, blocks;
   int G, groups, per, shift;      // heads per kv head; column groups, heads in one, log2 tokens
+  int inv_per;                    // ceil(256 / per): col * inv_per / 256 = col / per for col < 8
   FastDiv pd;
   float scale;
   int f[SA_MAX_OFFSETS];
@@ -124,22 +133,6 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
-// Lane layouts of a row of D elements, in pieces of at most 16 bytes of the
-// cache's type.
-//   K (and q): lane c of a quad holds KP pieces of KE elements, piece i at
-//              element (4 i + c) KE;
-//   V (and o): lane g of eight holds VP pieces of VE elements, piece i at
-//              element (8 i + g) VE.
-template <int D, bool E4M3>
-struct Lay {
-  static constexpr int kElt = E4M3 ? 1 : 2, kRow = D * kElt;      // bytes
-  static constexpr int kFull = 16 / kElt;
-  static constexpr int KE = D / 4 < kFull ? D / 4 : kFull, KP = D / 4 / KE;
-  static constexpr int VE = D / 8 < kFull ? D / 8 : kFull, VP = D / 8 / VE;
-  static constexpr int KW = D / 4 * kElt / 4;                     // words of a K part
-  static constexpr int VN = VE * kElt < 4 ? 1 : VE * kElt / 4;    // words of a V piece
-};
-
 // Two e4m3 codes as two fp16 values: exact, NaN kept.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   uint32_t h;
@@ -147,84 +140,149 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   return h;
 }
 
-// K parts of 16 rows: this lane's of rows g (a) and g + 8 (b) of the tile.
-template <int D, bool E4M3>
-struct KTile {
-  using Y = Lay<D, E4M3>;
-  uint32_t a[Y::KW], b[Y::KW];
-  __device__ __forceinline__ void load(const uint8_t* lane_base, int ra, int rb) {
-    const uint8_t* pa = lane_base + (int64_t)ra * Y::kRow;
-    const uint8_t* pb = lane_base + (int64_t)rb * Y::kRow;
-    constexpr int PB = Y::KE * Y::kElt;      // bytes of a piece
-#pragma unroll
-    for (int i = 0; i < Y::KP; ++i) {
-      load_words<PB>(pa + i * 4 * PB, a + i * (PB / 4));
-      load_words<PB>(pb + i * 4 * PB, b + i * (PB / 4));
-    }
-  }
-  // S^T of the 16 rows with the block's 8 columns
-  __device__ __forceinline__ void scores(const uint32_t (&q)[D / 8], float (&s)[4]) const {
-    s[0] = s[1] = s[2] = s[3] = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      if constexpr (E4M3)
-        mma16816<true>(s, e4m3x2_to_f16x2(a[i] & 0xffffu), e4m3x2_to_f16x2(b[i] & 0xffffu),
-                       e4m3x2_to_f16x2(a[i] >> 16), e4m3x2_to_f16x2(b[i] >> 16), q[2 * i],
-                       q[2 * i + 1]);
-      else
-        mma16816<false>(s, a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1], q[2 * i],
-                        q[2 * i + 1]);
-    }
-  }
-};
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+template <bool TRANS, int OFFSET>
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4 + %5];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr), "n"(OFFSET)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4 + %5];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr), "n"(OFFSET)
+                 : "memory");
+}
+__device__ __forceinline__ float load_shared(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
 
-// V parts of 16 rows: this lane's of rows 2c, 2c+1, 2c+8 and 2c+9 of the tile.
+// A stage: 32 gathered rows (two tiles of 16) of K or V, in 16-byte chunks whose
+// place is exchanged by row (so that eight rows of one chunk column, an ldmatrix
+// phase, fall into different banks), and for e4m3 rows their scales.
 template <int D, bool E4M3>
-struct VTile {
-  using Y = Lay<D, E4M3>;
-  uint32_t u[4][Y::VP * Y::VN];
-  __device__ __forceinline__ void load(const uint8_t* lane_base, int r, int row) {
-    const uint8_t* p = lane_base + (int64_t)row * Y::kRow;
-    constexpr int PB = Y::VE * Y::kElt;
-#pragma unroll
-    for (int i = 0; i < Y::VP; ++i) load_words<PB>(p + i * 8 * PB, u[r] + i * Y::VN);
+struct Stage {
+  static constexpr int kRow = D * (E4M3 ? 1 : 2);       // bytes
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kTile = 16 * kRow;
+  static constexpr int kScales = 2 * kTile;             // offset of the key scales, then the values'
+  static constexpr int kBytes = 2 * kTile + (E4M3 ? 256 : 0);
+  static __device__ __forceinline__ int place(int row, int chunk) {
+    constexpr int kPer = kChunks >= 8 ? 1 : 8 / kChunks;
+    constexpr int kMask = kChunks >= 8 ? 7 : kChunks - 1;
+    return row * kRow + ((chunk ^ ((row / kPer) & kMask)) << 4);
   }
-  // O^T += V^T P^T; p0 and p1: the fragments of P^T
-  __device__ __forceinline__ void add(uint32_t p0, uint32_t p1, float (&o)[D / 16][4]) const {
+  // Copies the rows that the lanes name (pool rows; lane = row of the stage). Of
+  // its place a lane keeps the part that does not depend on the pass (own = place
+  // of its chunk in pass 0); `pool` points at its chunk of row 0.
+  static __device__ __forceinline__ int own() {
+    const int lane = threadIdx.x & 31;
+    return place(lane / kChunks, lane % kChunks);
+  }
+  static __device__ __forceinline__ void fill(uint32_t stage, int own, const uint8_t* pool,
+                                              int row, bool two) {
+    constexpr int kRows = 32 / kChunks;      // rows of a pass
+    const int r0 = (threadIdx.x & 31) / kChunks;
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) {      // head dims 2j and 2j + 1 of this lane's list
-      if constexpr (E4M3) {
-        const int w = j / 2;
-        const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-        const uint32_t x = __byte_perm(u[0][w], u[1][w], sel);
-        const uint32_t y = __byte_perm(u[2][w], u[3][w], sel);
-        mma16816<true>(o[j], e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(x >> 16),
-                       e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(y >> 16), p0, p1);
-      } else {
-        mma16816<false>(o[j], __byte_perm(u[0][j], u[1][j], 0x5410),
-                        __byte_perm(u[0][j], u[1][j], 0x7632),
-                        __byte_perm(u[2][j], u[3][j], 0x5410),
-                        __byte_perm(u[2][j], u[3][j], 0x7632), p0, p1);
+    for (int i = 0; i < kChunks; ++i) {
+      if (i == kChunks / 2 && kChunks > 1 && !two) break;
+      constexpr int kMask = kChunks >= 8 ? 7 : 0;      // passes of fewer than 8 rows
+      const int turn = ((i * kRows) & kMask) << 4;
+      const int r = __shfl_sync(0xffffffffu, row, i * kRows + r0);
+      copy16(stage + (own ^ turn) + i * kRows * kRow, pool + (int64_t)r * kRow);
+    }
+  }
+  // Lane offset of an ldmatrix of K (matrices: row halves, then chunks) or V
+  // (chunks, then row halves); step s of the loop over chunk pairs is at ^ (s << 5).
+  static __device__ __forceinline__ uint32_t lane_at(bool v) {
+    const int lane = threadIdx.x & 31, mi = lane >> 3;
+    const int half = v ? mi >> 1 : mi & 1, chunk = v ? mi & 1 : mi >> 1;
+    return place((lane & 7) + 8 * half, kChunks > 1 ? chunk : 0);
+  }
+  // S^T of a tile's 16 keys with the block's 8 columns.
+  static __device__ __forceinline__ void scores(uint32_t stage, int tile, uint32_t at,
+                                                const uint32_t (&q)[D / 8], float (&s)[4]) {
+    s[0] = s[1] = s[2] = s[3] = 0.f;
+    if constexpr (!E4M3) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {      // 16 elements: two chunks
+        uint32_t r[4];
+        tile == 0 ? ldmatrix4<false, 0>(stage + (at ^ (i << 5)), r)
+                  : ldmatrix4<false, kTile>(stage + (at ^ (i << 5)), r);
+        mma16816<false>(s, r[0], r[1], r[2], r[3], q[2 * i], q[2 * i + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < (kChunks + 1) / 2; ++i) {      // 16 codes a chunk, two chunks
+        uint32_t r[4];
+        tile == 0 ? ldmatrix4<false, 0>(stage + (at ^ (i << 5)), r)
+                  : ldmatrix4<false, kTile>(stage + (at ^ (i << 5)), r);
+#pragma unroll
+        for (int j = 0; j < (kChunks > 1 ? 2 : 1); ++j)
+          mma16816<true>(s, e4m3x2_to_f16x2(r[2 * j] & 0xffffu),
+                         e4m3x2_to_f16x2(r[2 * j + 1] & 0xffffu), e4m3x2_to_f16x2(r[2 * j] >> 16),
+                         e4m3x2_to_f16x2(r[2 * j + 1] >> 16), q[4 * i + 2 * j],
+                         q[4 * i + 2 * j + 1]);
       }
     }
   }
-};
-
-// A lane's walk over the rows that one member has for consecutive tokens: one
-// more row per token, in the same page mostly.
-struct Walk {
-  int row, left;      // pool row of the last token served; rows after it in its page
+  // O^T += V^T P^T of a tile's 16 values; p0, p1: P^T for rows 0..7 and 8..15.
+  // Lane g's head dims of product j: 16 j + g and 16 j + 8 + g, for e4m3 rows
+  // 16 j + 2 g and the next.
+  static __device__ __forceinline__ void add(uint32_t stage, int tile, uint32_t at, uint32_t p0,
+                                             uint32_t p1, float (&o)[D / 16][4]) {
+    if constexpr (!E4M3) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t r[4];
+        tile == 0 ? ldmatrix4<true, 0>(stage + (at ^ (j << 5)), r)
+                  : ldmatrix4<true, kTile>(stage + (at ^ (j << 5)), r);
+        mma16816<false>(o[j], r[0], r[1], r[2], r[3], p0, p1);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < (kChunks + 1) / 2; ++i) {
+        uint32_t r[4];
+        tile == 0 ? ldmatrix4<true, 0>(stage + (at ^ (i << 5)), r)
+                  : ldmatrix4<true, kTile>(stage + (at ^ (i << 5)), r);
+#pragma unroll
+        for (int j = 0; j < (kChunks > 1 ? 2 : 1); ++j) {
+          // two rows of a pair of codes to two pairs of rows of a code
+          const uint32_t x = __byte_perm(r[j], 0, 0x3120), y = __byte_perm(r[2 + j], 0, 0x3120);
+          mma16816<true>(o[2 * i + j], e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(x >> 16),
+                         e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(y >> 16), p0, p1);
+        }
+      }
+    }
+  }
 };
 
 template <typename QT, int D, bool E4M3>
 __device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, int n, int b,
                                        int pos, bool inside);
 
+// A lane's walk over the pool rows that one member has for consecutive tokens:
+// mostly the next row of the same page.
+struct Walk {
+  int row = 0, left = -1;      // the last row, and how many follow it in its page
+};
+
 // ---------------------------------------------------------------------------
-// NT: pairs of offset tiles (16 offsets each), 0 .. 2.
+// NT: pairs of offset tiles (16 offsets each), 0 .. 2. Two stages per warp are in
+// flight: one more costs the L1 more than it hides (20 warps of 8 KB leave it 68 KB).
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kWarps * 32) k_chunk_tc(const __grid_constant__ ChunkArgs a) {
-  using Y = Lay<D, E4M3>;
+__global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
+    k_chunk_tc(const __grid_constant__ ChunkArgs a) {
+  using Y = Stage<D, E4M3>;
+  extern __shared__ __align__(1024) uint8_t s_stages[];
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int x = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (x >= a.blocks) return;
@@ -241,18 +299,6 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_tc(const __grid_constant_
   const bool inside = posl >= 0 && posl + count <= (long long)a.max_pages * a.pd.d;
   const int pos0 = inside ? (int)posl : 0;
 
-  // column 2c + e of this lane: token tok[e] of the block, query head head[e]
-  const int heads = min(a.per, a.G - grp * a.per);
-  int tok[2], head[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int col = 2 * c + e;
-    tok[e] = col / a.per;
-    const int hh = col - tok[e] * a.per;
-    head[e] = h * a.G + grp * a.per + hh;
-    if (hh >= heads || tok[e] >= count) tok[e] = -1;
-  }
-
   // offset geometry: lane k holds offset k
   int off_lo = 0, off_c = 0x7fffffff;
   float off_w = 0.f;
@@ -262,205 +308,257 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_tc(const __grid_constant_
     off_lo = og.lo; off_c = og.c; off_w = og.w;
     ok = ok && og.ok;
   }
+  ok = __all_sync(0xffffffffu, ok);
   const int* table = a.table + (size_t)b * a.max_pages;
   const size_t pool = (size_t)layer * a.n_pages * a.Hkv * a.pd.d;
-  const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.kc) + pool * Y::kRow + c * Y::KE * Y::kElt;
-  const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.vc) + pool * Y::kRow + g * Y::VE * Y::kElt;
+  const size_t chunk = pool * Y::kRow + (lane % Y::kChunks) * 16;      // this lane's, of row 0
+  const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.kc) + chunk;
+  const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.vc) + chunk;
   const float* ks = E4M3 ? a.ks + pool : nullptr;
   const float* vs = E4M3 ? a.vs + pool : nullptr;
   bool lost = !inside;      // a position or page outside its range
-  ok = __all_sync(0xffffffffu, ok);
 
-  // query fragments: column g of the block. For e4m3 rows in fp16, times a power
-  // of two that brings the column's largest element to [2^14, 2^15): an element
-  // loses bits only where it is 2^28 times smaller.
-  uint32_t q[D / 8];
+  // column 2c + e of this lane: token tok[e] of the block, query head sub[e] of the
+  // group, position qpos[e]
+  const int heads = min(a.per, a.G - grp * a.per), head0 = h * a.G + grp * a.per;
+  auto token_of = [&](int col) { return col * a.inv_per >> 8; };      // col / per, col < 8
+  int tok[2], sub[2], qpos[2];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) q[i] = 0u;
-  {
-    const int t = g / a.per, hh = g - t * a.per;
-    if (hh < heads && t < count) {
-      const __nv_bfloat16* qp = reinterpret_cast<const __nv_bfloat16*>(a.q) + layer * a.ql +
-                                (n0 + t) * a.qn + (h * a.G + grp * a.per + hh) * a.qh;
-#pragma unroll
-      for (int i = 0; i < Y::KP; ++i) {
-        const uint8_t* p = reinterpret_cast<const uint8_t*>(qp + (4 * i + c) * Y::KE);
-        if constexpr (Y::KE == 16) {
-          load_words<16>(p, q + i * 8);
-          load_words<16>(p + 16, q + i * 8 + 4);
-        } else {
-          load_words<Y::KE * 2>(p, q + i * (Y::KE / 2));
-        }
-      }
-    }
-  }
-  float scale[2] = {a.scale * kLog2e, a.scale * kLog2e};      // of the lane's two columns
-  if constexpr (E4M3) {
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-      top = fmaxf(top, fmaxf(fabsf(bf16lo(q[i])), fabsf(bf16hi(q[i]))));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    int e = (int)(__float_as_uint(top) >> 23) - 127;          // 2^e <= top < 2^(e+1)
-    e = e < -100 || e > 127 ? 14 : e;                         // zeros, infinities: as they are
-    const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-    const float down = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) q[i] = pack16<true>(bf16lo(q[i]) * up, bf16hi(q[i]) * up);
-    scale[0] *= __shfl_sync(0xffffffffu, down, 8 * c);
-    scale[1] *= __shfl_sync(0xffffffffu, down, 8 * c + 4);
-  }
-  float beta[2] = {0.f, 0.f};
-  if (a.beta) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (tok[e] >= 0)
-        beta[e] = kLog2e * __ldg(a.beta + ((size_t)layer * a.N + n0 + tok[e]) * a.Hq + head[e]);
+  for (int e = 0; e < 2; ++e) {
+    tok[e] = token_of(2 * c + e);
+    sub[e] = 2 * c + e - tok[e] * a.per;
+    if (sub[e] >= heads || tok[e] >= count) tok[e] = -1;
+    qpos[e] = tok[e] < 0 ? -(1 << 30) : pos0 + tok[e];
   }
 
-  // Running reference m and sum l of each of the lane's columns; o the outputs
-  // times l. For e4m3 rows the reference is the maximum of score + log2(value
-  // scale): the weights that go into P V, probability * value scale, are then at
-  // most 1 and fit fp16 whatever the scales.
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float o[D / 16][4];
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  float sig[NT > 0 ? 2 * NT : 1][2];
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_stages) +
+                        (threadIdx.x >> 5) * (2 * Y::kBytes);
+  const int hrow = h * a.pd.d, page_rows = a.Hkv * a.pd.d;
 
-  if (ok) {
+  auto run = [&](auto kind) {
+    constexpr bool FLAT = decltype(kind)::value;      // integer distances only
+    constexpr int STEP = FLAT ? 2 : 1;                // tokens of an offset stage
     auto find = [&](int r, int& left) {
       const int lp = quotient(a.pd, r), in = r - lp * a.pd.d;
-      const int page = __ldg(table + lp);
-      left = a.pd.d - 1 - in;
+      int page = __ldg(table + lp);
       if ((unsigned)page >= (unsigned)a.n_pages) {
         lost = true;
-        left = 0;
-        return 0;
+        page = 0;
       }
-      return (page * a.Hkv + h) * a.pd.d + in;
-    };
-    auto step_to = [&](Walk& w, int r, int by) {      // from row r - by to row r
-      if (w.left >= by) {
-        w.row += by;
-        w.left -= by;
-      } else {
-        w.row = find(r, w.left);
-      }
+      left = a.pd.d - 1 - in;
+      return page * page_rows + hrow + in;
     };
     // Rows without a member take this row, the first token's own, with weight 0.
     int unused;
     const int fill = find(pos0, unused);
-    const bool flat = __all_sync(0xffffffffu, off_w == 0.f);      // integer distances only
 
-    // ---- offset scores -------------------------------------------------------
-    // A tile pair serves 16 offsets. Interpolated: tile i holds, for 8 offsets,
-    // rows a in 0..7 and rows b in 8..15, and lane c of quad g looks up row a (c
-    // even) or b (c odd) of offset g of tile c / 2. Integer distances only: one
-    // tile per token holds 16 offsets; lanes 0..15 look up the rows of token t,
-    // lanes 16..31 those of t + 1.
-    int lo_[NT > 0 ? NT : 1], c_[NT > 0 ? NT : 1];
-    float w_[NT > 0 ? 2 * NT : 1];
-    bool two = true;
+    // ---- stages, in the order in which they are used: offset keys; window keys and
+    // values in turn; offset values ----
+    const int own = Y::own();
+    uint32_t in = ring, out = ring;
+    constexpr uint32_t kFlip = Y::kBytes;
+    auto stage_in = [&](const uint8_t* rows, int row, bool two, bool keys) {
+      Y::fill(in, own, rows, row, two);
+      if constexpr (E4M3) {
+        if (keys) copy4(in + Y::kScales + lane * 4, ks + row);
+        copy4(in + Y::kScales + 128 + lane * 4, vs + row);
+      }
+      in = ring + kFlip - (in - ring);
+    };
+    auto take = [&]() {      // the next stage to use, complete and visible to the warp
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      const uint32_t s = out;
+      out = ring + kFlip - (out - ring);
+      return s;
+    };
+    auto commit = []() { asm volatile("cp.async.commit_group;" ::: "memory"); };
+
+    // Offset stages. Interpolated: one per (token, tile pair); tile i of the pair
+    // has, for 8 offsets, rows a in 0..7 and rows b in 8..15. Integer distances: a
+    // tile holds 16 offsets of one token, a stage those of two tokens.
+    int lo_[NT > 0 ? NT : 1], c_[NT > 0 ? NT : 1];      // of the row this lane looks up
+    const int ahead = FLAT ? lane >> 4 : 0;             // for token t + ahead
 #pragma unroll
     for (int pair = 0; pair < NT; ++pair) {
-      const int src = pair * 16 + (flat ? lane & 15 : (c >> 1) * 8 + g);
-      const float w = __shfl_sync(0xffffffffu, off_w, src);
-      lo_[pair] = __shfl_sync(0xffffffffu, off_lo, src) + (flat ? 0 : c & 1);
+      const int src = pair * 16 + (FLAT ? lane & 15 : (lane >> 4) * 8 + (lane & 7));
+      const bool isb = !FLAT && (lane & 8);
+      lo_[pair] = __shfl_sync(0xffffffffu, off_lo, src) + isb;
       c_[pair] = __shfl_sync(0xffffffffu, off_c, src);
-      if (!flat && (c & 1) && w == 0.f) c_[pair] = 0x7fffffff;      // no second row
-      w_[2 * pair] = __shfl_sync(0xffffffffu, off_w, pair * 16 + g);
-      w_[2 * pair + 1] = __shfl_sync(0xffffffffu, off_w, pair * 16 + 8 + g);
+      if (!FLAT && __shfl_sync(0xffffffffu, off_w, src) == 0.f && isb)
+        c_[pair] = 0x7fffffff;      // no second row
     }
-    (void)two;
-    const int ahead = flat ? lane >> 4 : 0;       // this lane serves token t + ahead
-    const int stride = flat ? 2 : 1;
+    Walk walk[NT > 0 ? NT : 1];
+    int next_t = 0;      // token of the next offset stage
+    auto offset_in = [&](int pair, bool keys) {
+      const int mine = next_t + ahead, p = pos0 + mine;
+      const bool there = c_[pair] <= p && mine < count;
+      Walk& w = walk[pair];
+      if (there) {
+        w.row += STEP;
+        w.left -= STEP;
+        if (w.left < 0) w.row = find(p - lo_[pair], w.left);
+      }
+      stage_in(keys ? kb : vb, there ? w.row : fill,
+               FLAT ? next_t + 1 < count : pair * 16 + 8 < a.n_off, keys);
+      if (pair == NT - 1) next_t += STEP;
+    };
+    const int n_off = NT * ((count + STEP - 1) / STEP);
 
-    if constexpr (NT > 0) {
+    // Window tiles of 16 rows from `base`, the sinks as tile -1 before them.
+    const int last = pos0 + count - 1;
+    const int base = max(0, pos0 - (a.W - 1));
+    const int t_first = a.S > 0 ? -1 : 0, t_past = (last - base) / 16 + 1;
+    int win_row = 0, win_t = t_first;      // rows and first tile of the last key stage
+    auto window_in = [&](int t0, bool keys) {
+      if (keys) {
+        const int t = t0 + (lane >> 4);      // this lane's tile
+        const int r = (t < 0 ? 0 : base + t * 16) + (lane & 15);
+        const bool there = r <= last && (t >= 0 || r < a.S);
+        win_row = find(there ? r : pos0, unused);
+        win_t = t0;
+      }
+      stage_in(keys ? kb : vb, win_row, win_t + 1 < t_past, keys);
+    };
+    // stage k of the whole order for k = 0 and 1, and from then on two ahead
+    if constexpr (NT == 0) {
+      window_in(t_first, true); commit();
+      window_in(t_first, false); commit();
+    } else {
+      offset_in(0, true); commit();
+      if (n_off > 1) offset_in(NT - 1, true); else window_in(t_first, true);
+      commit();
+    }
+
+    // Query fragments of column g. For e4m3 rows in fp16, times a power of two that
+    // brings the column's largest element to [2^14, 2^15): an element loses bits
+    // only where it is 2^28 times smaller.
+    uint32_t q[D / 8];
 #pragma unroll
-      for (int i = 0; i < 2 * NT; ++i) sig[i][0] = sig[i][1] = -INFINITY;
-      Walk w[NT];
+    for (int i = 0; i < D / 8; ++i) q[i] = 0u;
+    {
+      const int t = token_of(g), hh = g - t * a.per;
+      if (hh < heads && t < count) {
+        const uint8_t* qp = reinterpret_cast<const uint8_t*>(
+            reinterpret_cast<const __nv_bfloat16*>(a.q) + layer * a.ql + (n0 + t) * a.qn +
+            (head0 + hh) * a.qh);
 #pragma unroll
-      for (int pair = 0; pair < NT; ++pair) w[pair] = {0, -1};
-      // scores of a tile, times its rows' scales; ra, rb < 0: no member
-      auto tile_scores = [&](const KTile<D, E4M3>& k, int ra, int rb, float (&s)[4]) {
-        k.scores(q, s);
-        if constexpr (E4M3) {
-          const float ka = __ldg(ks + (ra ^ (ra >> 31))), kc = __ldg(ks + (rb ^ (rb >> 31)));
-          s[0] *= ka; s[1] *= ka; s[2] *= kc; s[3] *= kc;
-        }
-      };
-      auto log_scale = [&](int r) {
-        return __log2f(fmaxf(fabsf(__ldg(vs + (r ^ (r >> 31)))), 7.9e-31f));
-      };
-      for (int t = 0; t < count; t += stride) {
-#pragma unroll
-        for (int pair = 0; pair < NT; ++pair) {
-          const int p = pos0 + t + ahead;
-          int row = ~fill;
-          if (c_[pair] <= p && t + ahead < count) {
-            step_to(w[pair], p - lo_[pair], stride);
-            row = w[pair].row;
-          }
-          if (flat) {
-            // tiles of tokens t and t + 1
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (t + i >= count) continue;
-              const int ra = __shfl_sync(0xffffffffu, row, i * 16 + g);
-              const int rb = __shfl_sync(0xffffffffu, row, i * 16 + 8 + g);
-              KTile<D, E4M3> k;
-              k.load(kb, ra ^ (ra >> 31), rb ^ (rb >> 31));
-              float s[4];
-              tile_scores(k, ra, rb, s);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                if (tok[e] == t + i) {
-                  if (ra >= 0) sig[2 * pair][e] = fmaf(s[e], scale[e], beta[e]);
-                  if (rb >= 0) sig[2 * pair + 1][e] = fmaf(s[2 + e], scale[e], beta[e]);
-                }
-              }
-              if constexpr (E4M3) {
-                const float va = log_scale(ra), vc = log_scale(rb);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (tok[e] == t + i)
-                    m[e] = fmaxf(m[e], fmaxf(sig[2 * pair][e] + va, sig[2 * pair + 1][e] + vc));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (i == 1 && pair * 16 + 8 >= a.n_off) continue;
-              const int ra = __shfl_sync(0xffffffffu, row, (lane & 28) + 2 * i);
-              const int rb = __shfl_sync(0xffffffffu, row, (lane & 28) + 2 * i + 1);
-              KTile<D, E4M3> k;
-              k.load(kb, ra ^ (ra >> 31), rb ^ (rb >> 31));
-              float s[4];
-              tile_scores(k, ra, rb, s);
-              const float wb = w_[2 * pair + i], wa = 1.f - wb;
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float y = rb >= 0 ? wa * s[e] + wb * s[2 + e] : s[e];
-                if (ra >= 0 && tok[e] == t) sig[2 * pair + i][e] = fmaf(y, scale[e], beta[e]);
-              }
-              if constexpr (E4M3) {
-                float va = log_scale(ra);
-                if (rb >= 0) va = fmaxf(va, log_scale(rb));
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (tok[e] == t) m[e] = fmaxf(m[e], sig[2 * pair + i][e] + va);
-              }
-            }
+        for (int i = 0; i < D / 16; ++i) {
+          if constexpr (E4M3) {      // elements 16 i + 4 c ..
+            load_words<8>(qp + i * 32 + c * 8, q + 2 * i);
+          } else {                   // 16 i + 2 c .. and 8 further
+            load_words<4>(qp + i * 32 + c * 4, q + 2 * i);
+            load_words<4>(qp + i * 32 + 16 + c * 4, q + 2 * i + 1);
           }
         }
       }
-      if constexpr (!E4M3) {
+    }
+    float scale[2] = {a.scale * kLog2e, a.scale * kLog2e};      // of the lane's two columns
+    if constexpr (E4M3) {
+      float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) {
-          m[0] = fmaxf(m[0], sig[i][0]);
-          m[1] = fmaxf(m[1], sig[i][1]);
+      for (int i = 0; i < D / 8; ++i)
+        top = fmaxf(top, fmaxf(fabsf(bf16lo(q[i])), fabsf(bf16hi(q[i]))));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      int e = (int)(__float_as_uint(top) >> 23) - 127;          // 2^e <= top < 2^(e+1)
+      e = e < -100 || e > 127 ? 14 : e;                         // zeros, infinities: as they are
+      const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+      const float down = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) q[i] = pack16<true>(bf16lo(q[i]) * up, bf16hi(q[i]) * up);
+      scale[0] *= __shfl_sync(0xffffffffu, down, 8 * c);
+      scale[1] *= __shfl_sync(0xffffffffu, down, 8 * c + 4);
+    }
+    const uint32_t at_k = Y::lane_at(false), at_v = Y::lane_at(true);
+    // scales of the stage's rows i * 16 + half * 8 + g: keys 0, values 1
+    auto row_scale = [&](uint32_t stage, int which, int i, int half) {
+      return load_shared(stage + Y::kScales + which * 128 + (i * 16 + half * 8 + g) * 4);
+    };
+    auto log_scale = [](float x) {      // 2^-100 at least; NaN does not matter here
+      float y;
+      asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(fabsf(x), 7.9e-31f)));
+      return y;
+    };
+
+    // Running reference m and sum l of each of the lane's columns; o the outputs
+    // times l. For e4m3 rows the reference is the maximum of score + log2(value
+    // scale): the weights that go into P V, probability * value scale, are then at
+    // most 1 and fit fp16 whatever the scales.
+    constexpr int NS = NT > 0 ? 2 * NT : 1;
+    [[maybe_unused]] float sig[NS][2], wg[NS];      // scores, and weights of row b, of offset 8 i + g
+    if constexpr (NT > 0) {
+      // ---- offset scores: a lane keeps its own columns' ----
+      float vl[NS][2];
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        wg[i] = FLAT ? 0.f : __shfl_sync(0xffffffffu, off_w, i * 8 + g);
+        sig[i][0] = sig[i][1] = vl[i][0] = vl[i][1] = 0.f;
+      }
+      int k = 2;      // the stage after the next
+      for (int t = 0; t < count; t += STEP) {
+#pragma unroll
+        for (int pair = 0; pair < NT; ++pair, ++k) {
+          const bool second = FLAT ? t + 1 < count : pair * 16 + 8 < a.n_off;
+          const uint32_t stage = take();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (i == 1 && !second) continue;
+            float s[4], va = 0.f, vc = 0.f, ka = 1.f, kc = 1.f;
+            Y::scores(stage, i, at_k, q, s);
+            if constexpr (E4M3) {
+              ka = row_scale(stage, 0, i, 0);
+              kc = row_scale(stage, 0, i, 1);
+              va = log_scale(row_scale(stage, 1, i, 0));
+              vc = log_scale(row_scale(stage, 1, i, 1));
+            }
+            if constexpr (FLAT) {      // rows g and g + 8: offsets 16 pair + g and + 8
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (tok[e] == t + i) {
+                  sig[2 * pair][e] = s[e] * ka;
+                  sig[2 * pair + 1][e] = s[2 + e] * kc;
+                  vl[2 * pair][e] = va;
+                  vl[2 * pair + 1][e] = vc;
+                }
+            } else {      // (a weight of 0 times a non-finite score: found at the end)
+              const float wb = wg[2 * pair + i] * kc, wa = (1.f - wg[2 * pair + i]) * ka;
+              if (wg[2 * pair + i] != 0.f) va = fmaxf(va, vc);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (tok[e] == t) {
+                  sig[2 * pair + i][e] = fmaf(wb, s[2 + e], wa * s[e]);
+                  vl[2 * pair + i][e] = va;
+                }
+            }
+          }
+          __syncwarp();
+          if (k < n_off)
+            offset_in(pair, true);
+          else
+            window_in(t_first, k == n_off);
+          commit();
+        }
+      }
+      float beta[2] = {0.f, 0.f};
+      if (a.beta) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (tok[e] >= 0)
+            beta[e] = kLog2e * __ldg(a.beta + ((size_t)layer * a.N + n0 + tok[e]) * a.Hq + head0 +
+                                     sub[e]);
+      }
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int cc = __shfl_sync(0xffffffffu, off_c, i * 8 + g);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sig[i][e] = cc <= qpos[e] ? fmaf(sig[i][e], scale[e], beta[e]) : -INFINITY;
+          m[e] = fmaxf(m[e], E4M3 ? sig[i][e] + vl[i][e] : sig[i][e]);
         }
       }
 #pragma unroll
@@ -468,72 +566,51 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_tc(const __grid_constant_
         m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], d));
         m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], d));
       }
+      next_t = 0;
+#pragma unroll
+      for (int pair = 0; pair < NT; ++pair) walk[pair] = Walk();
     }
 
-    // ---- sinks (tile -1) and window, two tiles of 16 rows at a time -------------
-    const int last = pos0 + count - 1;
-    const int base = max(0, pos0 - (a.W - 1));
-    const int tiles = (last - base) / 16 + 1;
-    for (int t0 = a.S > 0 ? -1 : 0; t0 < tiles; t0 += 2) {
-      const int mine = t0 + (lane >> 4);      // the tile this lane looks a row up for
-      const int r_ = mine < 0 ? lane & 15 : base + mine * 16 + (lane & 15);
-      const bool in = r_ <= last && (mine < 0 ? r_ < a.S : mine < tiles);
-      const int row = in ? find(r_, unused) : fill;
-      const bool second = t0 + 1 < tiles;
-      float s[2][4], lv[2][2];
-      int rk[2][2];
-      KTile<D, E4M3> k[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        rk[i][0] = __shfl_sync(0xffffffffu, row, i * 16 + g);
-        rk[i][1] = __shfl_sync(0xffffffffu, row, i * 16 + 8 + g);
-        if (i == 0 || second) k[i].load(kb, rk[i][0], rk[i][1]);
-      }
+    // ---- window and sinks, two tiles of 16 rows at a time ----
+    for (int t0 = t_first; t0 < t_past; t0 += 2) {
+      const bool second = t0 + 1 < t_past, more = t0 + 2 < t_past;
+      float s[2][4], nm[2] = {-INFINITY, -INFINITY};
+      uint32_t stage = take();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (i == 1 && !second) {
           s[1][0] = s[1][1] = s[1][2] = s[1][3] = -INFINITY;
           continue;
         }
-        k[i].scores(q, s[i]);
+        Y::scores(stage, i, at_k, q, s[i]);
         const int t = t0 + i;
-        float ka[2] = {scale[0], scale[1]}, kc[2] = {scale[0], scale[1]};
+        float ka[2] = {scale[0], scale[1]}, kc[2] = {scale[0], scale[1]}, va = 0.f, vc = 0.f;
         if constexpr (E4M3) {
-          const float x0 = __ldg(ks + rk[i][0]), x1 = __ldg(ks + rk[i][1]);
+          const float x0 = row_scale(stage, 0, i, 0), x1 = row_scale(stage, 0, i, 1);
           ka[0] *= x0; ka[1] *= x0; kc[0] *= x1; kc[1] *= x1;
+          va = log_scale(row_scale(stage, 1, i, 0));
+          vc = log_scale(row_scale(stage, 1, i, 1));
         }
-        // lags of rows r and r + 8 from the two columns' positions; sinks have no
-        // far edge but a last row
-        const int r = t < 0 ? g : base + t * 16 + g;
+        // lags of rows g and g + 8 from the two columns' positions (negative, so
+        // large unsigned, where there is no column); sinks have no far edge, and
+        // beyond the last one stand at a position past all
+        const int r0 = t < 0 ? (g < a.S ? g : 1 << 29) : base + t * 16 + g;
+        const int r1 = t < 0 ? (g + 8 < a.S ? g + 8 : 1 << 29) : r0 + 8;
         const unsigned far = t < 0 ? 0x7fffffffu : (unsigned)a.W;
-        const bool ea = t >= 0 || r < a.S, eb = t >= 0 || r + 8 < a.S;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int lag = pos0 + tok[e] - r;
-          const bool on = tok[e] >= 0;
-          s[i][e] = on && ea && (unsigned)lag < far ? s[i][e] * ka[e] : -INFINITY;
-          s[i][2 + e] = on && eb && (unsigned)(lag - 8) < far ? s[i][2 + e] * kc[e] : -INFINITY;
-        }
-        if constexpr (E4M3) {
-          lv[i][0] = __ldg(vs + rk[i][0]);
-          lv[i][1] = __ldg(vs + rk[i][1]);
+          s[i][e] = (unsigned)(qpos[e] - r0) < far ? s[i][e] * ka[e] : -INFINITY;
+          s[i][2 + e] = (unsigned)(qpos[e] - r1) < far ? s[i][2 + e] * kc[e] : -INFINITY;
+          nm[e] = fmaxf(nm[e], E4M3 ? fmaxf(s[i][e] + va, s[i][2 + e] + vc)
+                                    : fmaxf(s[i][e], s[i][2 + e]));
         }
       }
-      float nm[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if constexpr (E4M3) {
-          nm[e] = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (i == 0 || second) {
-              nm[e] = fmaxf(nm[e], s[i][e] + __log2f(fmaxf(fabsf(lv[i][0]), 7.9e-31f)));
-              nm[e] = fmaxf(nm[e], s[i][2 + e] + __log2f(fmaxf(fabsf(lv[i][1]), 7.9e-31f)));
-            }
-        } else {
-          nm[e] = fmaxf(fmaxf(s[0][e], s[0][2 + e]), fmaxf(s[1][e], s[1][2 + e]));
-        }
-      }
+      __syncwarp();
+      if (more)
+        window_in(t0 + 2, true);
+      else if (NT > 0)
+        offset_in(0, false);
+      commit();
 #pragma unroll
       for (int d = 4; d <= 16; d <<= 1) {
         nm[0] = fmaxf(nm[0], __shfl_xor_sync(0xffffffffu, nm[0], d));
@@ -554,91 +631,86 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_tc(const __grid_constant_
         }
       }
       const float z0 = m[0] == -INFINITY ? 0.f : m[0], z1 = m[1] == -INFINITY ? 0.f : m[1];
+      stage = take();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (i == 1 && !second) continue;
-        VTile<D, E4M3> v;
-        v.load(vb, 0, __shfl_sync(0xffffffffu, row, i * 16 + 2 * c));
-        v.load(vb, 1, __shfl_sync(0xffffffffu, row, i * 16 + 2 * c + 1));
-        v.load(vb, 2, __shfl_sync(0xffffffffu, row, i * 16 + 2 * c + 8));
-        v.load(vb, 3, __shfl_sync(0xffffffffu, row, i * 16 + 2 * c + 9));
         float p[4] = {exp2_approx(s[i][0] - z0), exp2_approx(s[i][1] - z1),
                       exp2_approx(s[i][2] - z0), exp2_approx(s[i][3] - z1)};
         l[0] += p[0] + p[2];
         l[1] += p[1] + p[3];
         if constexpr (E4M3) {
-          p[0] = s[i][0] == -INFINITY ? 0.f : p[0] * lv[i][0];
-          p[1] = s[i][1] == -INFINITY ? 0.f : p[1] * lv[i][0];
-          p[2] = s[i][2] == -INFINITY ? 0.f : p[2] * lv[i][1];
-          p[3] = s[i][3] == -INFINITY ? 0.f : p[3] * lv[i][1];
+          const float va = row_scale(stage, 1, i, 0), vc = row_scale(stage, 1, i, 1);
+          p[0] *= va; p[1] *= va; p[2] *= vc; p[3] *= vc;
         }
-        v.add(transpose8(pack16<E4M3>(p[0], p[1])), transpose8(pack16<E4M3>(p[2], p[3])), o);
+        Y::add(stage, i, at_v, transpose8(pack16<E4M3>(p[0], p[1])),
+               transpose8(pack16<E4M3>(p[2], p[3])), o);
       }
+      __syncwarp();
+      if (more)
+        window_in(t0 + 2, false);
+      else if (n_off > 1)
+        offset_in(NT - 1, false);
+      commit();
     }
 
-    // ---- offset values -----------------------------------------------------------
+    // ---- offset values ----
     if constexpr (NT > 0) {
       const float z0 = m[0] == -INFINITY ? 0.f : m[0], z1 = m[1] == -INFINITY ? 0.f : m[1];
+      // P^T of all columns (plain rows): lane (g, c) has column g, rows 2c and 2c + 1;
+      // a token's product takes its own columns of it
+      [[maybe_unused]] uint32_t pa[NS], pb[NS];
+      const int tok_g = token_of(g);
 #pragma unroll
-      for (int i = 0; i < 2 * NT; ++i) {
+      for (int i = 0; i < NS; ++i) {
         sig[i][0] = exp2_approx(sig[i][0] - z0);
         sig[i][1] = exp2_approx(sig[i][1] - z1);
         l[0] += sig[i][0];
         l[1] += sig[i][1];
+        if constexpr (!E4M3) {
+          const float wb = wg[i], wa = 1.f - wb;
+          pa[i] = transpose8(pack_bf16x2(sig[i][0] * wa, sig[i][1] * wa));
+          if (!FLAT) pb[i] = transpose8(pack_bf16x2(sig[i][0] * wb, sig[i][1] * wb));
+        }
       }
-      Walk w[NT];
+      int k = 2;
+      for (int t = 0; t < count; t += STEP) {
 #pragma unroll
-      for (int pair = 0; pair < NT; ++pair) w[pair] = {0, -1};
-      for (int t = 0; t < count; t += stride) {
-#pragma unroll
-        for (int pair = 0; pair < NT; ++pair) {
-          const int p = pos0 + t + ahead;
-          int row = fill;
-          if (c_[pair] <= p && t + ahead < count) {
-            step_to(w[pair], p - lo_[pair], stride);
-            row = w[pair].row;
-          }
+        for (int pair = 0; pair < NT; ++pair, ++k) {
+          const bool second = FLAT ? t + 1 < count : pair * 16 + 8 < a.n_off;
+          const uint32_t stage = take();
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            // interpolated: tile i of the pair; flat: the tile of token t + i
-            if (flat ? t + i >= count : (i == 1 && pair * 16 + 8 >= a.n_off)) continue;
-            const int s0 = flat ? i * 16 + 2 * c : 8 * c + 2 * i;
-            const int dn = flat ? 1 : 4, db = flat ? 8 : 1;      // next row; row + 8
-            VTile<D, E4M3> v;
-            v.load(vb, 0, __shfl_sync(0xffffffffu, row, s0));
-            v.load(vb, 1, __shfl_sync(0xffffffffu, row, s0 + dn));
-            v.load(vb, 2, __shfl_sync(0xffffffffu, row, s0 + db));
-            v.load(vb, 3, __shfl_sync(0xffffffffu, row, s0 + dn + db));
-            const int at = flat ? t + i : t;
-            const bool on0 = tok[0] == at, on1 = tok[1] == at;
-            float pa0, pa1, pb0, pb1;
-            if (flat) {
-              pa0 = sig[2 * pair][0]; pa1 = sig[2 * pair][1];
-              pb0 = sig[2 * pair + 1][0]; pb1 = sig[2 * pair + 1][1];
-            } else {
-              const float wb = w_[2 * pair + i], wa = 1.f - wb;
-              pa0 = sig[2 * pair + i][0]; pa1 = sig[2 * pair + i][1];
-              pb0 = pa0 * wb; pb1 = pa1 * wb;
-              pa0 *= wa; pa1 *= wa;
-            }
+            if (i == 1 && !second) continue;
+            const int at = FLAT ? t + i : t;
+            const int ia = FLAT ? 2 * pair : 2 * pair + i, ib = FLAT ? 2 * pair + 1 : ia;
+            uint32_t p0, p1;
             if constexpr (E4M3) {
-              const float va = __ldg(vs + __shfl_sync(0xffffffffu, row,
-                                                      flat ? i * 16 + g : (lane & 28) + 2 * i));
-              const float vc = __ldg(vs + __shfl_sync(0xffffffffu, row,
-                                                      flat ? i * 16 + 8 + g
-                                                           : (lane & 28) + 2 * i + 1));
-              pa0 = pa0 == 0.f ? 0.f : pa0 * va;
-              pa1 = pa1 == 0.f ? 0.f : pa1 * va;
-              pb0 = pb0 == 0.f ? 0.f : pb0 * vc;
-              pb1 = pb1 == 0.f ? 0.f : pb1 * vc;
+              const float wb = FLAT ? 1.f : wg[ia], wa = FLAT ? 1.f : 1.f - wb;
+              const float va = row_scale(stage, 1, i, 0) * wa, vc = row_scale(stage, 1, i, 1) * wb;
+              const bool on0 = tok[0] == at, on1 = tok[1] == at;
+              p0 = transpose8(pack16<true>(on0 ? sig[ia][0] * va : 0.f, on1 ? sig[ia][1] * va : 0.f));
+              p1 = transpose8(pack16<true>(on0 ? sig[ib][0] * vc : 0.f, on1 ? sig[ib][1] * vc : 0.f));
+            } else {
+              p0 = tok_g == at ? pa[ia] : 0u;
+              p1 = tok_g == at ? (FLAT ? pa[ib] : pb[ib]) : 0u;
             }
-            v.add(transpose8(pack16<E4M3>(on0 ? pa0 : 0.f, on1 ? pa1 : 0.f)),
-                  transpose8(pack16<E4M3>(on0 ? pb0 : 0.f, on1 ? pb1 : 0.f)), o);
+            Y::add(stage, i, at_v, p0, p1, o);
           }
+          __syncwarp();
+          if (k < n_off) offset_in(pair, false);
+          commit();
         }
       }
     }
+  };
+  if (ok) {
+    if (NT > 0 && !__all_sync(0xffffffffu, off_w == 0.f))
+      run(std::false_type());
+    else
+      run(std::true_type());
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
   for (int d = 4; d <= 16; d <<= 1) {
     l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
@@ -648,40 +720,62 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_tc(const __grid_constant_
 
   // A weight of 0 does not hide an infinity or a NaN: when an output is not
   // finite, the block's queries are computed again from their own members alone.
-  float odd = 0.f;      // x - x is 0 for finite x only
+  float odd[2] = {l[0], l[1]};      // times 0: 0 for finite values only
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j) {
-    if (tok[0] >= 0) odd += (o[j][0] - o[j][0]) + (o[j][2] - o[j][2]);
-    if (tok[1] >= 0) odd += (o[j][1] - o[j][1]) + (o[j][3] - o[j][3]);
+  for (int e = 0; e < 2; ++e) {
+    odd[e] *= 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+      odd[e] = fmaf(o[j][e], 0.f, fmaf(o[j][2 + e], 0.f, odd[e]));
   }
-  if (!nan && __any_sync(0xffffffffu, odd != 0.f)) {
+  if (!nan && __any_sync(0xffffffffu, (tok[0] >= 0 && odd[0] != 0.f) ||
+                                          (tok[1] >= 0 && odd[1] != 0.f))) {
     for (int col = 0; col < count * a.per; ++col) {
-      const int t = col / a.per, hh = col - t * a.per;
+      const int t = token_of(col), hh = col - t * a.per;
       if (hh < heads)
-        one_query<__nv_bfloat16, D, E4M3>(a, layer, h * a.G + grp * a.per + hh, n0 + t, b,
-                                          pos0 + t, true);
+        one_query<__nv_bfloat16, D, E4M3>(a, layer, head0 + hh, n0 + t, b, pos0 + t, true);
     }
     return;
   }
 
+  // Outputs through shared memory: one row per column, 16 bytes apart in banks,
+  // then 16 bytes a lane of consecutive head dims.
+  constexpr int kOut = D * 2 + 16;
+  uint8_t* out = s_stages + (threadIdx.x >> 5) * (2 * Y::kBytes);
+  static_assert(8 * kOut <= 2 * Y::kBytes, "the output tile fits the stages");
+  __syncwarp();
+  const float bad = __int_as_float(0x7fc00000);
+  const float inv0 = nan ? bad : 1.f / l[0], inv1 = nan ? bad : 1.f / l[1];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    if (tok[e] < 0) continue;
-    const size_t at = ((size_t)layer * a.N + n0 + tok[e]) * a.Hq + head[e];
-    const float bad = __int_as_float(0x7fc00000);
-    const float inv = nan ? bad : 1.f / l[e];
-    __nv_bfloat16* op = reinterpret_cast<__nv_bfloat16*>(a.o) + at * D;
-#pragma unroll
-    for (int i = 0; i < Y::VP; ++i) {
-      float y[Y::VE];
-#pragma unroll
-      for (int j = 0; j < Y::VE / 2; ++j) {
-        y[2 * j] = o[i * (Y::VE / 2) + j][e] * inv;
-        y[2 * j + 1] = o[i * (Y::VE / 2) + j][2 + e] * inv;
-      }
-      store_row<__nv_bfloat16, Y::VE>(op + (8 * i + g) * Y::VE, y);
+  for (int j = 0; j < D / 16; ++j) {
+    if constexpr (E4M3) {      // head dims 16 j + 2 g and the next
+      *reinterpret_cast<uint32_t*>(out + (2 * c) * kOut + (16 * j + 2 * g) * 2) =
+          pack_bf16x2(o[j][0] * inv0, o[j][2] * inv0);
+      *reinterpret_cast<uint32_t*>(out + (2 * c + 1) * kOut + (16 * j + 2 * g) * 2) =
+          pack_bf16x2(o[j][1] * inv1, o[j][3] * inv1);
+    } else {                   // transposed: column g, head dims 2c and 2c + 1 of eight
+      *reinterpret_cast<uint32_t*>(out + g * kOut + (16 * j + 2 * c) * 2) =
+          transpose8(pack_bf16x2(o[j][0] * inv0, o[j][1] * inv1));
+      *reinterpret_cast<uint32_t*>(out + g * kOut + (16 * j + 8 + 2 * c) * 2) =
+          transpose8(pack_bf16x2(o[j][2] * inv0, o[j][3] * inv1));
     }
-    if (g == 0 && a.lse) a.lse[at] = nan ? bad : kLn2 * (m[e] + log2f(l[e]));
+  }
+  __syncwarp();
+  constexpr int kPer = D / 8;      // 16-byte chunks of a row
+  const size_t out0 = ((size_t)layer * a.N + n0) * a.Hq + head0;
+#pragma unroll
+  for (int i = 0; i < 8 * kPer / 32 || i == 0; ++i) {
+    const int id = i * 32 + lane, col = id / kPer, t = token_of(col), hh = col - t * a.per;
+    if (id < 8 * kPer && t < count && hh < heads)
+      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o) +
+                                (out0 + t * a.Hq + hh) * D + (id % kPer) * 8) =
+          *reinterpret_cast<const uint4*>(out + col * kOut + (id % kPer) * 16);
+  }
+  if (a.lse && g == 0) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (tok[e] >= 0)
+        a.lse[out0 + tok[e] * a.Hq + sub[e]] = nan ? bad : kLn2 * (m[e] + log2f(l[e]));
   }
   if (__any_sync(0xffffffffu, lost) && lane == 0) atomicOr(&g_chunk_err, kErrPage);
 }
@@ -883,23 +977,33 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const __grid_constant
   one_query<float, D, E4M3>(a, blockIdx.z, blockIdx.y, n, b, inside ? (int)posl : 0, inside);
 }
 
+template <int D, bool E4M3, int NT>
+cudaError_t launch_tc(const ChunkArgs& a, const dim3& grid, cudaStream_t st) {
+  constexpr int smem = kWarps * 2 * Stage<D, E4M3>::kBytes;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_chunk_tc<D, E4M3, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  k_chunk_tc<D, E4M3, NT><<<grid, kWarps * 32, smem, st>>>(a);
+  return cudaSuccess;
+}
+
 template <int D, bool E4M3>
 cudaError_t launch_t(const ChunkArgs& a, bool f32, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
   trace_mark("chunk_attn", st, true);
   if (f32) {
     const dim3 grid((a.N + kWarps - 1) / kWarps, a.Hq, a.L);
     k_chunk_f32<D, E4M3><<<grid, kWarps * 32, 0, st>>>(a);
   } else {
     const dim3 grid((a.blocks + kWarps - 1) / kWarps, a.Hkv * a.groups, a.L);
-    if (a.n_off == 0)
-      k_chunk_tc<D, E4M3, 0><<<grid, kWarps * 32, 0, st>>>(a);
-    else if (a.n_off <= 16)
-      k_chunk_tc<D, E4M3, 1><<<grid, kWarps * 32, 0, st>>>(a);
-    else
-      k_chunk_tc<D, E4M3, 2><<<grid, kWarps * 32, 0, st>>>(a);
+    e = a.n_off == 0 ? launch_tc<D, E4M3, 0>(a, grid, st)
+        : a.n_off <= 16 ? launch_tc<D, E4M3, 1>(a, grid, st)
+                        : launch_tc<D, E4M3, 2>(a, grid, st);
   }
   trace_mark("chunk_attn", st, false);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -922,6 +1026,7 @@ cudaError_t launch_chunk_attn(const PagedProblem& p, const PagedPtrs& c, const C
   a.G = p.Hq / p.Hkv;
   a.groups = (a.G + 7) / 8;
   a.per = (a.G + a.groups - 1) / a.groups;
+  a.inv_per = (256 + a.per - 1) / a.per;
   a.shift = a.per == 1 ? 3 : (a.per == 2 ? 2 : (a.per <= 4 ? 1 : 0));
   a.blocks = a.shift ? (p.N >> a.shift) + p.B : p.N;
   const bool f32 = p.dtype == SA_DTYPE_F32, q8 = p.format == SA_CACHE_E4M3;
