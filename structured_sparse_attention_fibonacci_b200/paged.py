@@ -14,10 +14,12 @@ arguments are checked here or in the library before anything is launched.
     O, lse = chunk_attn(q, cache, page_table, cu_q, cached, alpha, window=12)
 
 All tensors of a call are on one CUDA device, which need not be the current
-one; the work goes to that device's current stream, or to ``stream``.
+one; the work goes to that device's current stream, or to ``stream=`` (every
+call takes it).
 """
 import contextlib
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -73,49 +75,63 @@ def paged_cache(layers, n_pages, heads, page_size, head_dim, dtype=torch.bfloat1
                               for _ in range(2)))
 
 
+# Single calls of this module take a few microseconds of kernel time, so what a
+# call does in Python counts: devices are compared by index and the stream is
+# taken as the raw handle.
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _empty_like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _addr(t):
     return t.data_ptr() if t is not None else None
 
 
 @contextlib.contextmanager
-def _entered(dev, stream):
-    with torch.cuda.device(dev), (contextlib.nullcontext() if stream is None
-                                  else torch.cuda.stream(stream)):
+def _entered(index, stream):
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream must be on cuda:{index}")
+    with torch.cuda.device(index), (contextlib.nullcontext() if stream is None
+                                    else torch.cuda.stream(stream)):
         yield
 
 
-def _on(dev, stream):
-    """Makes dev (and stream) current for the call's allocations and launches."""
-    if stream is None and torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext()
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream must be on {dev}")
-    return _entered(dev, stream)
+def _on_its_device(call):
+    """Runs call(first, ..., stream=) with the device of its first tensor current
+    and stream (of that device) its current stream: allocations and launches go there."""
+    @functools.wraps(call)
+    def wrapped(first, *args, stream=None, **kw):
+        t = first.k if isinstance(first, PagedCache) else first
+        index = t.get_device()
+        if index < 0:
+            raise ValueError("the tensors must be on a CUDA device")
+        if stream is None and _current_device() == index:
+            return call(first, *args, **kw)
+        with _entered(index, stream):
+            return call(first, *args, **kw)
+    return wrapped
 
 
-def _stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
-
-
-def _device(t, name):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
-
-
-def _whole(name, t, shape, dtype, dev):
+def _whole(name, t, shape, dtype, index):
     """t: a contiguous tensor of that shape, type and device."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+    if (t.dtype != dtype or t.shape != shape or t.get_device() != index
+            or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
-                         f"on {dev}")
+                         f"on cuda:{index}")
 
 
-def _rows(name, t, shape, dtype, dev, kind):
-    """t: rows of that shape, their elements contiguous; its strides."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev or t.stride(-1) != 1:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {dev} with "
-                         "contiguous rows")
-    return kind(*[s if n > 1 else 0 for s, n in zip(t.stride()[:-1], shape[:-1])])
+def _rows(name, t, shape, dtype, index, kind):
+    """t: rows of that shape, their elements contiguous; its strides (0 where there
+    is one)."""
+    strides = t.stride()
+    if (t.dtype != dtype or t.shape != shape or t.get_device() != index or strides[-1] != 1):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on "
+                         f"cuda:{index} with contiguous rows")
+    return kind(*[s if n > 1 else 0 for s, n in zip(strides[:-1], shape)])
 
 
 def _span(t):
@@ -126,8 +142,8 @@ def _span(t):
 def _output(name, out, like, others):
     """out, checked, or a new contiguous tensor like `like`."""
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    _whole(name, out, like.shape, like.dtype, like.device)
+        return _empty_like(like)
+    _whole(name, out, like.shape, like.dtype, like.get_device())
     _apart(name, out, like, others)
     return out
 
@@ -147,7 +163,7 @@ def _apart(name, out, own, others):
 
 # ---- norms of queries and keys ------------------------------------------------
 def _norm_args(q, k, q_weight, k_weight, eps, rotate, rope_base, pos0):
-    dev = _device(q, "q")
+    dev = q.get_device()
     if q.dim() != 5 or k.dim() != 5:
         raise ValueError("q and k must be [L, B, H, T, D]")
     if q.dtype not in _DTYPES:
@@ -168,8 +184,9 @@ def _norm_args(q, k, q_weight, k_weight, eps, rotate, rope_base, pos0):
     return dev, p, qs, ks
 
 
+@_on_its_device
 def qk_norm_rope(q, k, q_weight, k_weight, *, eps=1e-6, rotate=True, rope_base=10000.0, pos0=0,
-                 q_out=None, k_out=None, stream=None):
+                 q_out=None, k_out=None):
     """RMS norm of every query and key head, and the position rotation, in one
     pass (sparse_attn_qk_norm_rope): returns contiguous (q', k').
 
@@ -180,19 +197,19 @@ def qk_norm_rope(q, k, q_weight, k_weight, *, eps=1e-6, rotate=True, rope_base=1
     and decode() rotate by themselves).  q_out may be a contiguous q, k_out a
     contiguous k."""
     dev, p, qs, ks = _norm_args(q, k, q_weight, k_weight, eps, rotate, rope_base, pos0)
-    with _on(dev, stream):
-        q_out = _output("q_out", q_out, q, (k, k_out))
-        k_out = _output("k_out", k_out, k, (q,))
-        _check("sparse_attn_qk_norm_rope",
-               lib().sparse_attn_qk_norm_rope(p, _addr(q), qs, _addr(k), ks, _addr(q_weight),
-                                              _addr(k_weight), _addr(q_out), _addr(k_out),
-                                              _stream(dev)))
+    q_out = _output("q_out", q_out, q, (k, k_out))
+    k_out = _output("k_out", k_out, k, (q,))
+    _check("sparse_attn_qk_norm_rope",
+           lib().sparse_attn_qk_norm_rope(p, _addr(q), qs, _addr(k), ks, _addr(q_weight),
+                                          _addr(k_weight), _addr(q_out), _addr(k_out),
+                                          _raw_stream(dev)))
     return q_out, k_out
 
 
+@_on_its_device
 def qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, *, eps=1e-6, rotate=True,
                      rope_base=10000.0, pos0=0, dq=None, dk=None, dq_weight=None, dk_weight=None,
-                     workspace=None, stream=None):
+                     workspace=None):
     """Gradients of qk_norm_rope for its outputs' gradients dq_out, dk_out
     (shaped like q and k, rows contiguous): returns contiguous (dq, dk) and the
     fp32 [L, D] gradients of the weights (None, None without weights), summed in a
@@ -202,25 +219,24 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, *, eps=1e-6, rota
     dev, p, qs, ks = _norm_args(q, k, q_weight, k_weight, eps, rotate, rope_base, pos0)
     dqs = _rows("dq_out", dq_out, q.shape, q.dtype, dev, HeadStrides)
     dks = _rows("dk_out", dk_out, k.shape, k.dtype, dev, HeadStrides)
-    with _on(dev, stream):
-        dq = _output("dq", dq, dq_out, (q, k, dk_out, dk))
-        dk = _output("dk", dk, dk_out, (q, k, dq_out))
-        if q_weight is not None:
-            dq_weight = _output("dq_weight", dq_weight, q_weight, ())
-            dk_weight = _output("dk_weight", dk_weight, k_weight, (dq_weight,))
+    dq = _output("dq", dq, dq_out, (q, k, dk_out, dk))
+    dk = _output("dk", dk, dk_out, (q, k, dq_out))
+    if q_weight is not None:
+        dq_weight = _output("dq_weight", dq_weight, q_weight, ())
+        dk_weight = _output("dk_weight", dk_weight, k_weight, (dq_weight,))
+        if workspace is None:
             need = int(lib().sparse_attn_qk_norm_workspace_size(p))
-            if workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            elif workspace.device != dev or not workspace.is_contiguous():
-                raise ValueError(f"workspace must be a contiguous buffer on {dev}")
-        elif dq_weight is not None or dk_weight is not None:
-            raise ValueError("no weights, no gradients of them")
-        n = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check("sparse_attn_qk_norm_rope_bwd",
-               lib().sparse_attn_qk_norm_rope_bwd(
-                   p, _addr(q), qs, _addr(k), ks, _addr(q_weight), _addr(k_weight), _addr(dq_out),
-                   dqs, _addr(dk_out), dks, _addr(dq), _addr(dk), _addr(dq_weight),
-                   _addr(dk_weight), _addr(workspace), n, _stream(dev)))
+            workspace = q.new_empty(need, dtype=torch.uint8)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous buffer on cuda:{dev}")
+    elif dq_weight is not None or dk_weight is not None:
+        raise ValueError("no weights, no gradients of them")
+    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("sparse_attn_qk_norm_rope_bwd",
+           lib().sparse_attn_qk_norm_rope_bwd(
+               p, _addr(q), qs, _addr(k), ks, _addr(q_weight), _addr(k_weight), _addr(dq_out),
+               dqs, _addr(dk_out), dks, _addr(dq), _addr(dk), _addr(dq_weight),
+               _addr(dk_weight), _addr(workspace), n, _raw_stream(dev)))
     return dq, dk, dq_weight, dk_weight
 
 
@@ -233,8 +249,10 @@ def qk_norm_workspace_size(q_shape, k_shape, dtype=torch.bfloat16) -> int:
 
 # ---- paged cache ----------------------------------------------------------------
 def _paged_args(cache, page_table, dtype, L_, N, Hq):
-    k, v = cache.k, cache.v
-    dev = _device(k, "cache.k")
+    k, v, k_scale, v_scale = cache
+    dev = k.get_device()
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
     if k.dim() != 5:
         raise ValueError("cache.k must be [L, n_pages, Hkv, page_size, D]")
     _, n_pages, Hkv, page_size, D = k.shape
@@ -246,11 +264,11 @@ def _paged_args(cache, page_table, dtype, L_, N, Hq):
     _whole("cache.k", k, shape, k.dtype, dev)
     _whole("cache.v", v, shape, k.dtype, dev)
     if quantised:
-        if cache.k_scale is None or cache.v_scale is None:
+        if k_scale is None or v_scale is None:
             raise ValueError("float8_e4m3fn pages need k_scale and v_scale")
-        _whole("cache.k_scale", cache.k_scale, shape[:4], torch.float32, dev)
-        _whole("cache.v_scale", cache.v_scale, shape[:4], torch.float32, dev)
-    elif cache.k_scale is not None or cache.v_scale is not None:
+        _whole("cache.k_scale", k_scale, shape[:4], torch.float32, dev)
+        _whole("cache.v_scale", v_scale, shape[:4], torch.float32, dev)
+    elif k_scale is not None or v_scale is not None:
         raise ValueError("scales belong to float8_e4m3fn pages only")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
@@ -258,7 +276,7 @@ def _paged_args(cache, page_table, dtype, L_, N, Hq):
     _whole("page_table", page_table, (B, max_pages), torch.int32, dev)
     p = PagedParams(L_, N, B, Hkv if Hq is None else Hq, Hkv, D, n_pages, page_size, max_pages,
                     _DTYPES[dtype], SA_CACHE_E4M3 if quantised else SA_CACHE_PLAIN)
-    c = Pages(_addr(k), _addr(v), _addr(cache.k_scale), _addr(cache.v_scale), _addr(page_table))
+    c = Pages(k.data_ptr(), v.data_ptr(), _addr(k_scale), _addr(v_scale), page_table.data_ptr())
     return dev, p, c
 
 
@@ -267,8 +285,9 @@ def _sequences(cu_q, cached, B, dev):
     _whole("cached", cached, (B,), torch.int32, dev)
 
 
+@_on_its_device
 def cache_append(q, k, v, cache, page_table, cu_q, cached, *, q_weight=None, k_weight=None,
-                 eps=1e-6, rope_base=10000.0, q_out=None, stream=None):
+                 eps=1e-6, rope_base=10000.0, q_out=None):
     """Writes new tokens into the cache (sparse_attn_cache_append): their keys
     rotated (and normed, with weights), their values as they are, both quantised
     for float8_e4m3fn pages; returns their rotated queries [L, N, Hq, D].
@@ -294,21 +313,21 @@ def cache_append(q, k, v, cache, page_table, cu_q, cached, *, q_weight=None, k_w
     if q_weight is not None:
         _whole("q_weight", q_weight, (L_, D), torch.float32, dev)
         _whole("k_weight", k_weight, (L_, D), torch.float32, dev)
-    with _on(dev, stream):
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        else:
-            _whole("q_out", q_out, q.shape, q.dtype, dev)
-            _apart("q_out", q_out, None, (q, k, v))
-        _check("sparse_attn_cache_append",
-               lib().sparse_attn_cache_append(
-                   p, c, _addr(cu_q), _addr(cached), _addr(q), qs, _addr(k), ks, _addr(v), vs,
-                   _addr(q_weight), _addr(k_weight), eps, rope_base, _addr(q_out), _stream(dev)))
+    if q_out is None:
+        q_out = _empty_like(q)
+    else:
+        _whole("q_out", q_out, q.shape, q.dtype, dev)
+        _apart("q_out", q_out, None, (q, k, v))
+    _check("sparse_attn_cache_append",
+           lib().sparse_attn_cache_append(
+               p, c, cu_q.data_ptr(), cached.data_ptr(), q.data_ptr(), qs, k.data_ptr(), ks,
+               v.data_ptr(), vs, _addr(q_weight), _addr(k_weight), eps, rope_base,
+               q_out.data_ptr(), _raw_stream(dev)))
     return q_out
 
 
-def cache_read(cache, page_table, lengths, *, rows=None, dtype=None, k_out=None, v_out=None,
-               stream=None):
+@_on_its_device
+def cache_read(cache, page_table, lengths, *, rows=None, dtype=None, k_out=None, v_out=None):
     """The first lengths[b] rows of every sequence (int32 [B]) as contiguous
     (k, v) [L, B, Hkv, rows, D] (sparse_attn_cache_read): the stored, rotated keys
     and the values; float8_e4m3fn pages are read as dtype (bf16 by default).
@@ -326,21 +345,21 @@ def cache_read(cache, page_table, lengths, *, rows=None, dtype=None, k_out=None,
     shape = (p.L, p.B, p.Hkv, rows, p.D)
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out: both or neither")
-    with _on(dev, stream):
-        if k_out is None:
-            k_out, v_out = (torch.zeros(shape, dtype=dtype, device=dev) for _ in range(2))
-        else:
-            _whole("k_out", k_out, shape, dtype, dev)
-            _whole("v_out", v_out, shape, dtype, dev)
-            _apart("v_out", v_out, None, (k_out,))
-        _check("sparse_attn_cache_read",
-               lib().sparse_attn_cache_read(p, c, _addr(lengths), rows, _addr(k_out),
-                                            _addr(v_out), _stream(dev)))
+    if k_out is None:
+        k_out, v_out = (cache.k.new_zeros(shape, dtype=dtype) for _ in range(2))
+    else:
+        _whole("k_out", k_out, shape, dtype, dev)
+        _whole("v_out", v_out, shape, dtype, dev)
+        _apart("v_out", v_out, None, (k_out,))
+    _check("sparse_attn_cache_read",
+           lib().sparse_attn_cache_read(p, c, lengths.data_ptr(), rows, k_out.data_ptr(),
+                                        v_out.data_ptr(), _raw_stream(dev)))
     return k_out, v_out
 
 
+@_on_its_device
 def chunk_attn(q, cache, page_table, cu_q, cached, alpha, *, window, offsets=FIB15, sinks=0,
-               scale=0.0, beta=None, out=None, lse=None, want_lse=True, stream=None):
+               scale=0.0, beta=None, out=None, lse=None, want_lse=True):
     """Sparse attention of new tokens over the paged cache, which holds their own
     rows already (sparse_attn_chunk): returns (O [L, N, Hq, D], LSE [L, N, Hq] or
     None).  One token per sequence is a decode step, many are a prefill chunk, and
@@ -360,24 +379,27 @@ def chunk_attn(q, cache, page_table, cu_q, cached, alpha, *, window, offsets=FIB
     _whole("alpha", alpha, (L_,), torch.float32, dev)
     if beta is not None:
         _whole("beta", beta, (L_, N, Hq), torch.float32, dev)
-    n_off = len(offsets)
-    offs = (ctypes.c_int32 * max(1, n_off))(*offsets)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        else:
-            _whole("out", out, q.shape, q.dtype, dev)
-            _apart("out", out, None, (q,))
-        if lse is not None:
-            _whole("lse", lse, (L_, N, Hq), torch.float32, dev)
-        elif want_lse:
-            lse = torch.empty((L_, N, Hq), dtype=torch.float32, device=dev)
-        _check("sparse_attn_chunk",
-               lib().sparse_attn_chunk(p, c, _addr(cu_q), _addr(cached), _addr(q), qs,
-                                       _addr(alpha), _addr(beta), int(window), n_off, offs,
-                                       int(sinks), float(scale), _addr(out), _addr(lse),
-                                       _stream(dev)))
+    if out is None:
+        out = _empty_like(q)
+    else:
+        _whole("out", out, q.shape, q.dtype, dev)
+        _apart("out", out, None, (q,))
+    if lse is not None:
+        _whole("lse", lse, (L_, N, Hq), torch.float32, dev)
+    elif want_lse:
+        lse = alpha.new_empty((L_, N, Hq))
+    offs = _offsets(tuple(offsets))
+    _check("sparse_attn_chunk",
+           lib().sparse_attn_chunk(p, c, cu_q.data_ptr(), cached.data_ptr(), q.data_ptr(), qs,
+                                   alpha.data_ptr(), _addr(beta), window, len(offs), offs, sinks,
+                                   scale, out.data_ptr(), _addr(lse), _raw_stream(dev)))
     return out, lse
+
+
+@functools.lru_cache(maxsize=64)
+def _offsets(offsets):
+    """The offset table as a C array (copied by the library during the call)."""
+    return (ctypes.c_int32 * len(offsets))(*[int(x) for x in offsets])
 
 
 def _bind(L):
