@@ -39,11 +39,34 @@ struct AppendArgs {
   void* q_out; void* kc; void* vc; float* ks; float* vs;
 };
 
+// 16 elements of a row as they lie in memory: 8 from p, 8 from p + half.
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, int half, float (&x1)[8], float (&x2)[8]) {
-  load_row<T, 8>(p, x1);
-  load_row<T, 8>(p + half, x2);
-}
+struct Raw {
+  static constexpr int kChunks = sizeof(T) / 2;      // 16-byte chunks of 8 elements
+  uint4 u[2][kChunks];
+  __device__ __forceinline__ void load(const T* p, int half) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      u[0][c] = __ldg(reinterpret_cast<const uint4*>(p) + c);
+      u[1][c] = __ldg(reinterpret_cast<const uint4*>(p + half) + c);
+    }
+  }
+  __device__ __forceinline__ void get(int i, float (&x)[8]) const {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const uint32_t w[4] = {u[i][c].x, u[i][c].y, u[i][c].z, u[i][c].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) {
+          x[4 * c + e] = __uint_as_float(w[e]);
+        } else {
+          x[2 * e] = bf16lo(w[e]);
+          x[2 * e + 1] = bf16hi(w[e]);
+        }
+      }
+    }
+  }
+};
 
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
@@ -67,6 +90,28 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_cache_append(const Append
   if (wid >= (long long)a.N * a.parts) return;
   const int n = (int)(wid / a.parts), part = (int)(wid % a.parts);
   const int j0 = sub * 8;
+  const int rows = a.Hq + 2 * a.Hkv, stride = a.parts * ROWS;
+  const T* q = reinterpret_cast<const T*>(a.q) + layer * a.ql + n * a.qn + j0;
+  const T* k = reinterpret_cast<const T*>(a.k) + layer * a.kl + n * a.kn + j0;
+  const T* v = reinterpret_cast<const T*>(a.v) + layer * a.vl + n * a.vn + j0;
+  // Rows in turn: q heads, k heads, v heads. Every group of the warp takes part in
+  // the shuffles; one without a row takes the last one again and does not store it.
+  // kBatch rows' loads are in flight at a time, the first ones before the sequence
+  // is known.
+  constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
+  Raw<T> raw[kBatch];
+  auto fetch_rows = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = min(r0 + i * stride + grp, rows - 1);
+      if (r0 + i * stride < rows)      // uniform
+        raw[i].load(r < a.Hq           ? q + r * a.qh
+                    : r < a.Hq + a.Hkv ? k + (r - a.Hq) * a.kh
+                                       : v + (r - a.Hq - a.Hkv) * a.vh,
+                    HALF);
+    }
+  };
+  fetch_rows(part * ROWS);
 
   const int b = find_sequence(a.cu, a.B, 0, n);
   const int first = __ldg(a.cu + b);
@@ -88,77 +133,76 @@ __global__ void __launch_bounds__(kAppendWarps * 32) k_cache_append(const Append
 #pragma unroll
     for (int i = 0; i < 8; ++i) cs[i] = make_float2(__int_as_float(0x7fc00000), 0.f);
   }
-  const int rows = a.Hq + 2 * a.Hkv;
   const int slot = (int)pos - lp * a.pd.d;
-  const T* q = reinterpret_cast<const T*>(a.q) + layer * a.ql + n * a.qn;
-  const T* k = reinterpret_cast<const T*>(a.k) + layer * a.kl + n * a.kn;
-  const T* v = reinterpret_cast<const T*>(a.v) + layer * a.vl + n * a.vn;
 
-  // every group of the warp takes part in the shuffles; a group without a row
-  // recomputes the last one and does not store it
-#pragma unroll 2
-  for (int r0 = part * ROWS; r0 < rows; r0 += a.parts * ROWS) {
-    const bool live = r0 + grp < rows;
-    const int r = min(r0 + grp, rows - 1);
-    const int what = r < a.Hq ? 0 : (r < a.Hq + a.Hkv ? 1 : 2);       // q, k, v
-    const int h = what == 0 ? r : (what == 1 ? r - a.Hq : r - a.Hq - a.Hkv);
-    const T* src = what == 0 ? q + h * a.qh : (what == 1 ? k + h * a.kh : v + h * a.vh);
-    float x1[8], x2[8];
-    load16<T>(src + j0, HALF, x1, x2);
-    if constexpr (NORM) {
-      float ss = 0.f;
+  for (int base = part * ROWS; base < rows; base += kBatch * stride) {
+    if (base > part * ROWS) fetch_rows(base);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x1[i], x1[i], fmaf(x2[i], x2[i], ss));
-      ss = group_sum<LANES>(ss);
-      if (what < 2) {
-        const float* w = (what == 0 ? a.qw : a.kw) + (size_t)layer * D + j0;
-        float w1[8], w2[8];
-        load_row<float, 8>(w, w1);
-        load_row<float, 8>(w + HALF, w2);
-        const float rstd = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+    for (int i = 0; i < kBatch; ++i) {
+      const int r0 = base + i * stride;
+      if (r0 >= rows) continue;      // uniform
+      const bool live = r0 + grp < rows;
+      const int r = min(r0 + grp, rows - 1);
+      const int what = r < a.Hq ? 0 : (r < a.Hq + a.Hkv ? 1 : 2);       // q, k, v
+      const int h = what == 0 ? r : (what == 1 ? r - a.Hq : r - a.Hq - a.Hkv);
+      float x1[8], x2[8];
+      raw[i].get(0, x1);
+      raw[i].get(1, x2);
+      if constexpr (NORM) {
+        float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x1[i] = x1[i] * rstd * w1[i];
-          x2[i] = x2[i] * rstd * w2[i];
+        for (int i = 0; i < 8; ++i) ss = fmaf(x1[i], x1[i], fmaf(x2[i], x2[i], ss));
+        ss = group_sum<LANES>(ss);
+        if (what < 2) {
+          const float* w = (what == 0 ? a.qw : a.kw) + (size_t)layer * D + j0;
+          float w1[8], w2[8];
+          load_row<float, 8>(w, w1);
+          load_row<float, 8>(w + HALF, w2);
+          const float rstd = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x1[i] = x1[i] * rstd * w1[i];
+            x2[i] = x2[i] * rstd * w2[i];
+          }
         }
       }
-    }
-    if (what < 2) rope_fwd<8>(x1, x2, cs);
-    if (what == 0) {
-      if (live) {
-        T* dst = reinterpret_cast<T*>(a.q_out) + (((size_t)layer * a.N + n) * a.Hq + h) * D + j0;
-        store_row<T, 8>(dst, x1);
-        store_row<T, 8>(dst + HALF, x2);
+      if (what < 2) rope_fwd<8>(x1, x2, cs);
+      if (what == 0) {
+        if (live) {
+          T* dst = reinterpret_cast<T*>(a.q_out) + (((size_t)layer * a.N + n) * a.Hq + h) * D + j0;
+          store_row<T, 8>(dst, x1);
+          store_row<T, 8>(dst + HALF, x2);
+        }
       }
-    }
-    float scale = 1.f;
-    if constexpr (E4M3) {
-      float m = 0.f;
-      bool nan = false;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m = fmaxf(m, fmaxf(fabsf(x1[i]), fabsf(x2[i])));
-        nan |= x1[i] != x1[i] || x2[i] != x2[i];
-      }
-      scale = e4m3_scale(group_max<LANES>(nan ? INFINITY : m));
-    }
-    if (what > 0 && live && have) {
-      const size_t row = (((size_t)layer * a.n_pages + page) * a.Hkv + h) * a.pd.d + slot;
+      float scale = 1.f;
       if constexpr (E4M3) {
-        const float inv = 1.f / scale;     // a power of two: exact
-        uint8_t* dst = reinterpret_cast<uint8_t*>(what == 1 ? a.kc : a.vc) + row * D + j0;
-        uint2 u;
-        u.x = float4_to_e4m3x4(x1[0] * inv, x1[1] * inv, x1[2] * inv, x1[3] * inv);
-        u.y = float4_to_e4m3x4(x1[4] * inv, x1[5] * inv, x1[6] * inv, x1[7] * inv);
-        *reinterpret_cast<uint2*>(dst) = u;
-        u.x = float4_to_e4m3x4(x2[0] * inv, x2[1] * inv, x2[2] * inv, x2[3] * inv);
-        u.y = float4_to_e4m3x4(x2[4] * inv, x2[5] * inv, x2[6] * inv, x2[7] * inv);
-        *reinterpret_cast<uint2*>(dst + HALF) = u;
-        if (sub == 0) (what == 1 ? a.ks : a.vs)[row] = scale;
-      } else {
-        T* dst = reinterpret_cast<T*>(what == 1 ? a.kc : a.vc) + row * D + j0;
-        store_row<T, 8>(dst, x1);
-        store_row<T, 8>(dst + HALF, x2);
+        float m = 0.f;
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          m = fmaxf(m, fmaxf(fabsf(x1[i]), fabsf(x2[i])));
+          nan |= x1[i] != x1[i] || x2[i] != x2[i];
+        }
+        scale = e4m3_scale(group_max<LANES>(nan ? INFINITY : m));
+      }
+      if (what > 0 && live && have) {
+        const size_t row = (((size_t)layer * a.n_pages + page) * a.Hkv + h) * a.pd.d + slot;
+        if constexpr (E4M3) {
+          const float inv = 1.f / scale;     // a power of two: exact
+          uint8_t* dst = reinterpret_cast<uint8_t*>(what == 1 ? a.kc : a.vc) + row * D + j0;
+          uint2 u;
+          u.x = float4_to_e4m3x4(x1[0] * inv, x1[1] * inv, x1[2] * inv, x1[3] * inv);
+          u.y = float4_to_e4m3x4(x1[4] * inv, x1[5] * inv, x1[6] * inv, x1[7] * inv);
+          *reinterpret_cast<uint2*>(dst) = u;
+          u.x = float4_to_e4m3x4(x2[0] * inv, x2[1] * inv, x2[2] * inv, x2[3] * inv);
+          u.y = float4_to_e4m3x4(x2[4] * inv, x2[5] * inv, x2[6] * inv, x2[7] * inv);
+          *reinterpret_cast<uint2*>(dst + HALF) = u;
+          if (sub == 0) (what == 1 ? a.ks : a.vs)[row] = scale;
+        } else {
+          T* dst = reinterpret_cast<T*>(what == 1 ? a.kc : a.vc) + row * D + j0;
+          store_row<T, 8>(dst, x1);
+          store_row<T, 8>(dst + HALF, x2);
+        }
       }
     }
   }

@@ -101,11 +101,39 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm(const NormArgs a) {
   }
 }
 
+// A thread's copies in flight: its own 16-byte chunks of the next rows' x and dy, in
+// slots of shared memory that no other thread touches (so no barrier is needed).
+// Registers would hold 16 KB an SM in flight beside the 100 that the arithmetic
+// takes; at 1 us of latency 6.5 TB/s need 44 KB.
+template <typename T>
+struct Ahead {
+  static constexpr int kChunks = sizeof(T) / 2 * 4;       // of x1, x2, dy1, dy2
+  static constexpr int kStages = sizeof(T) == 2 ? 4 : 3;
+  static constexpr int kBytes = kStages * kChunks * kThreads * 16;
+};
+
+template <typename T>
+__device__ __forceinline__ void read8(const uint8_t* slot, float (&x)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(slot);
+  if constexpr (sizeof(T) == 2) {
+    x[0] = bf16lo(u.x); x[1] = bf16hi(u.x); x[2] = bf16lo(u.y); x[3] = bf16hi(u.y);
+    x[4] = bf16lo(u.z); x[5] = bf16hi(u.z); x[6] = bf16lo(u.w); x[7] = bf16hi(u.w);
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(slot + kThreads * 16);
+    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+    x[4] = __uint_as_float(v.x); x[5] = __uint_as_float(v.y);
+    x[6] = __uint_as_float(v.z); x[7] = __uint_as_float(v.w);
+  }
+}
+
 // CTAs 0 .. n_q - 1 of a layer take q, the rest k; each a run of consecutive
 // (token tile, head) items, so that a tile's cosines serve its heads.
 template <typename T, int D, bool NORM, bool ROT>
-__global__ void __launch_bounds__(kThreads) k_qk_norm_bwd(const NormArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) k_qk_norm_bwd(const NormArgs a) {
   constexpr int LANES = D / 16, HALF = D / 2, PER = kThreads / LANES;
+  using Y = Ahead<T>;
+  extern __shared__ __align__(16) uint8_t s_ring[];
   __shared__ float s_part[kThreads / 32][D];
   const int sub = threadIdx.x % LANES, j0 = sub * 8, layer = blockIdx.y;
   const bool is_k = (int)blockIdx.x >= a.n_q;
@@ -128,28 +156,67 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_bwd(const NormArgs a) {
   }
   const long long items = (long long)((a.tokens + PER - 1) / PER) * H;
   const long long i0 = items * blk / blks, i1 = items * (blk + 1) / blks;
-  int tile = (int)(i0 / H), h = (int)(i0 - (long long)tile * H);
-  int b = 0, t = 0;
-  bool live = false, moved = true;
-  float2 cs[8];
-#pragma unroll 2
-  for (long long it = i0; it < i1; ++it) {
-    if (moved) {
-      const int p = tile * PER + threadIdx.x / LANES;
-      live = p < a.tokens;
-      const int pc = live ? p : a.tokens - 1;
-      b = pc / a.T;
-      t = pc - b * a.T;
-      if constexpr (ROT) load_cs<8>(a.rope + (size_t)(a.pos0 + t) * HALF + j0, cs);
-      moved = false;
+
+  // A walk over the items; b, t: this lane group's token (the last one again, and
+  // not live, behind the end).
+  struct At {
+    int tile, h, b, t;
+    bool live;
+  };
+  auto place = [&](At& p) {
+    const int n = p.tile * PER + threadIdx.x / LANES;
+    p.live = n < a.tokens;
+    const int c = p.live ? n : a.tokens - 1;
+    p.b = c / a.T;
+    p.t = c - p.b * a.T;
+  };
+  auto step = [&](At& p) {      // whether the tile changed
+    if (++p.h < H) return false;
+    p.h = 0;
+    ++p.tile;
+    place(p);
+    return true;
+  };
+  At in;
+  in.tile = (int)(i0 / H);
+  in.h = (int)(i0 - (long long)in.tile * H);
+  place(in);
+  At at = in;
+  long long next = i0;
+  int slot_in = 0, slot = 0;
+  auto issue = [&]() {
+    if (next < i1) {
+      const T* xp = x + in.b * s.batch + in.h * s.head + in.t * s.row;
+      const T* gp = dy + in.b * ds.batch + in.h * ds.head + in.t * ds.row;
+      const uint32_t dst = (uint32_t)__cvta_generic_to_shared(s_ring) +
+                           (slot_in * Y::kChunks * kThreads + threadIdx.x) * 16;
+      const T* part[4] = {xp, xp + HALF, gp, gp + HALF};
+#pragma unroll
+      for (int c = 0; c < Y::kChunks; ++c)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + c * kThreads * 16),
+                     "l"(part[c / (Y::kChunks / 4)] + (c % (Y::kChunks / 4)) * (16 / (int)sizeof(T)))
+                     : "memory");
+      step(in);
+      slot_in = slot_in + 1 == Y::kStages ? 0 : slot_in + 1;
     }
-    const T* xp = x + b * s.batch + h * s.head + t * s.row;
-    const T* gp = dy + b * ds.batch + h * ds.head + t * ds.row;
+    ++next;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < Y::kStages - 1; ++i) issue();
+  float2 cs[8];
+  if constexpr (ROT) load_cs<8>(a.rope + (size_t)(a.pos0 + at.t) * HALF + j0, cs);
+  for (long long it = i0; it < i1; ++it) {
+    issue();      // into the slot that the last round has read
+    asm volatile("cp.async.wait_group %0;" ::"n"(Y::kStages - 1) : "memory");
+    const uint8_t* from = s_ring + (slot * Y::kChunks * kThreads + threadIdx.x) * 16;
+    slot = slot + 1 == Y::kStages ? 0 : slot + 1;
     float x1[8], x2[8], g1[8], g2[8];
-    load_row<T, 8>(xp, x1);
-    load_row<T, 8>(xp + HALF, x2);
-    load_row<T, 8>(gp, g1);
-    load_row<T, 8>(gp + HALF, g2);
+    constexpr int kHalf = Y::kChunks / 4 * kThreads * 16;
+    read8<T>(from, x1);
+    read8<T>(from + kHalf, x2);
+    read8<T>(from + 2 * kHalf, g1);
+    read8<T>(from + 3 * kHalf, g2);
     if constexpr (ROT) rope_bwd<8>(g1, g2, cs);
     if constexpr (NORM) {
       float ss = 0.f, sg = 0.f;
@@ -165,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_bwd(const NormArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float n1 = x1[i] * r, n2 = x2[i] * r;
-        if (live) {
+        if (at.live) {
           dw1[i] = fmaf(g1[i], n1, dw1[i]);
           dw2[i] = fmaf(g2[i], n2, dw2[i]);
         }
@@ -173,16 +240,13 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_bwd(const NormArgs a) {
         g2[i] = r * (g2[i] * w2[i] - n2 * mean);
       }
     }
-    if (live) {
-      T* dst = dx + (((size_t)b * H + h) * a.T + t) * D;
+    if (at.live) {
+      T* dst = dx + (((size_t)at.b * H + at.h) * a.T + at.t) * D;
       store_row<T, 8>(dst, g1);
       store_row<T, 8>(dst + HALF, g2);
     }
-    if (++h == H) {
-      h = 0;
-      ++tile;
-      moved = true;
-    }
+    const bool moved = step(at);
+    if (ROT && moved) load_cs<8>(a.rope + (size_t)(a.pos0 + at.t) * HALF + j0, cs);
   }
   if constexpr (NORM) {
 #pragma unroll
@@ -210,12 +274,13 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_bwd(const NormArgs a) {
   }
 }
 
-// dw of one (layer, tensor): 256 / D slices add every (256 / D)-th partial, then
+// dw of one (layer, tensor): 1024 / D slices add every (1024 / D)-th partial, then
 // meet in shared memory.
+constexpr int kDwThreads = 1024;
 template <int D>
-__global__ void __launch_bounds__(kThreads) k_qk_norm_dw(const float* part, int n_q, int blocks,
+__global__ void __launch_bounds__(kDwThreads) k_qk_norm_dw(const float* part, int n_q, int blocks,
                                                          float* dqw, float* dkw) {
-  constexpr int SL = kThreads / D;
+  constexpr int SL = kDwThreads / D;
   __shared__ double s_sum[SL][D];
   const int layer = blockIdx.y, d = threadIdx.x % D, sl = threadIdx.x / D;
   const bool is_k = blockIdx.x == 1;
@@ -232,15 +297,20 @@ __global__ void __launch_bounds__(kThreads) k_qk_norm_dw(const float* part, int 
   }
 }
 
-// CTAs per layer of the backward: four resident per SM over all layers, not more
-// than there are items; at least one per tensor.
+// CTAs per layer of the backward: 1 to 4 times the 296 that the GPU holds, over all
+// layers, so that a CTA has 16 items or more where there are that many; at least
+// one per tensor. Long runs even out over several waves (16 x 8 x (8 + 8) x 1024 rows
+// of 64: 164 us with one wave, 141 with two, 130 with four), short ones pay for
+// each CTA's start and partial sums (2 x 3 x (12 + 4) x 777 rows of 128: 18, 21, 26).
 struct BwdGrid {
   int n_q, blocks;
 };
 BwdGrid bwd_grid(const NormProblem& p) {
   const long long per = kThreads / (p.D / 16);
   const long long tiles = ((long long)p.B * p.T + per - 1) / per;
-  const long long want = std::max(2LL, (148LL * 4 + p.L - 1) / p.L);
+  const long long waves =
+      std::min(4LL, std::max(1LL, tiles * (p.Hq + p.Hkv) * p.L / (296 * 16)));
+  const long long want = std::max(2LL, (296 * waves + p.L - 1) / p.L);
   const long long q = std::max(1LL, std::min(tiles * p.Hq, want * p.Hq / (p.Hq + p.Hkv)));
   const long long k = std::max(1LL, std::min(tiles * p.Hkv, want - want * p.Hq / (p.Hq + p.Hkv)));
   return {(int)q, (int)(q + k)};
@@ -273,12 +343,16 @@ cudaError_t bwd_v(const NormProblem& p, const NormArgs& a, float* dqw, float* dk
                   int* launches) {
   const BwdGrid g = bwd_grid(p);
   trace_mark("qk_norm_rope_bwd", st, true);
-  k_qk_norm_bwd<T, D, NORM, ROT><<<dim3(g.blocks, p.L), kThreads, 0, st>>>(a);
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_qk_norm_bwd<T, D, NORM, ROT>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, Ahead<T>::kBytes);
+  if (e != cudaSuccess) return e;
+  k_qk_norm_bwd<T, D, NORM, ROT><<<dim3(g.blocks, p.L), kThreads, Ahead<T>::kBytes, st>>>(a);
   trace_mark("qk_norm_rope_bwd", st, false);
   ++*launches;
   if constexpr (NORM) {
     trace_mark("qk_norm_dw", st, true);
-    k_qk_norm_dw<D><<<dim3(2, p.L), kThreads, 0, st>>>(a.part, g.n_q, g.blocks, dqw, dkw);
+    k_qk_norm_dw<D><<<dim3(2, p.L), kDwThreads, 0, st>>>(a.part, g.n_q, g.blocks, dqw, dkw);
     trace_mark("qk_norm_dw", st, false);
     ++*launches;
   }
