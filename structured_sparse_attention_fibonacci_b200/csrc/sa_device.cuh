@@ -170,6 +170,21 @@ __device__ __forceinline__ void load_cs(const float2* __restrict__ p, float2 (&c
   }
 }
 
+// 1 / sqrt(x) to about an ulp: the approximate instruction and one Newton step
+// (r (3 - x r^2) / 2), which zeros and infinities do without.
+__device__ __forceinline__ float inverse_sqrt(float x) {
+  const float r = rsqrtf(x);
+  const float y = fmaf(fmaf(x * r, -r, 1.f), 0.5f * r, r);
+  return x > 0.f && x < INFINITY ? y : r;
+}
+
+// Maximum that is NaN where an argument is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // Sum over the 8 lanes of a lane group (lanes 8g .. 8g+7); every lane of the
 // warp must call it.
 __device__ __forceinline__ float group8_sum(float v) {

@@ -49,7 +49,7 @@ __device__ __forceinline__ float inverse_rms(const float (&x1)[8], const float (
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s = fmaf(x1[i], x1[i], fmaf(x2[i], x2[i], s));
-  return 1.f / sqrtf(row_sum<D / 16>(s) * (1.f / D) + eps);
+  return inverse_sqrt(row_sum<D / 16>(s) * (1.f / D) + eps);
 }
 
 template <typename T, int D, bool NORM, bool ROT>
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_norm_bwd(const NormArgs a) {
       }
       ss = row_sum<LANES>(ss);
       sg = row_sum<LANES>(sg);
-      const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+      const float r = inverse_sqrt(ss * (1.f / D) + a.eps);
       const float mean = sg * r * (1.f / D);                 // of g w n
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
