@@ -133,11 +133,12 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
-// Two e4m3 codes as two fp16 values: exact, NaN kept.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t h;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"(two));
-  return h;
+// Four e4m3 codes as two pairs of fp16 values: exact, NaN kept.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; "
+      "cvt.rn.f16x2.e4m3x2 %1, b; }"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -226,11 +227,12 @@ struct Stage {
         tile == 0 ? ldmatrix4<false, 0>(stage + (at ^ (i << 5)), r)
                   : ldmatrix4<false, kTile>(stage + (at ^ (i << 5)), r);
 #pragma unroll
-        for (int j = 0; j < (kChunks > 1 ? 2 : 1); ++j)
-          mma16816<true>(s, e4m3x2_to_f16x2(r[2 * j] & 0xffffu),
-                         e4m3x2_to_f16x2(r[2 * j + 1] & 0xffffu), e4m3x2_to_f16x2(r[2 * j] >> 16),
-                         e4m3x2_to_f16x2(r[2 * j + 1] >> 16), q[4 * i + 2 * j],
-                         q[4 * i + 2 * j + 1]);
+        for (int j = 0; j < (kChunks > 1 ? 2 : 1); ++j) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x4(r[2 * j], a0, a2);
+          e4m3x4_to_f16x4(r[2 * j + 1], a1, a3);
+          mma16816<true>(s, a0, a1, a2, a3, q[4 * i + 2 * j], q[4 * i + 2 * j + 1]);
+        }
       }
     }
   }
@@ -256,9 +258,10 @@ struct Stage {
 #pragma unroll
         for (int j = 0; j < (kChunks > 1 ? 2 : 1); ++j) {
           // two rows of a pair of codes to two pairs of rows of a code
-          const uint32_t x = __byte_perm(r[j], 0, 0x3120), y = __byte_perm(r[2 + j], 0, 0x3120);
-          mma16816<true>(o[2 * i + j], e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(x >> 16),
-                         e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(y >> 16), p0, p1);
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x4(__byte_perm(r[j], 0, 0x3120), a0, a1);
+          e4m3x4_to_f16x4(__byte_perm(r[2 + j], 0, 0x3120), a2, a3);
+          mma16816<true>(o[2 * i + j], a0, a1, a2, a3, p0, p1);
         }
       }
     }
@@ -459,10 +462,11 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
     }
     float scale[2] = {a.scale * kLog2e, a.scale * kLog2e};      // of the lane's two columns
     if constexpr (E4M3) {
-      float top = 0.f;
+      __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
-        top = fmaxf(top, fmaxf(fabsf(bf16lo(q[i])), fabsf(bf16hi(q[i]))));
+        top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&q[i])));
+      float top = fmaxf(__low2float(top2), __high2float(top2));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       int e = (int)(__float_as_uint(top) >> 23) - 127;          // 2^e <= top < 2^(e+1)
