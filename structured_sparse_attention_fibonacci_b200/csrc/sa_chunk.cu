@@ -51,18 +51,13 @@ namespace {
 __device__ unsigned g_chunk_err;
 
 constexpr int kWarps = 4;
-#ifndef MB128
-#define MB128 4
-#endif
-#ifndef MB64
-#define MB64 4
-#endif
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct ChunkArgs {
   int L, N, B, Hq, Hkv, n_pages, max_pages, W, n_off, S, blocks;
   int G, groups, per, shift;      // heads per kv head; column groups, heads in one, log2 tokens
+  bool team;                      // a CTA's warps share a block
   int inv_per;                    // ceil(256 / per): col * inv_per / 256 = col / per for col < 8
   FastDiv pd;
   float scale;
@@ -279,15 +274,16 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------------------
-// NT: pairs of offset tiles (16 offsets each), 0 .. 2. Two stages per warp are in
+// NT: pairs of offset tiles (16 offsets each), 0 .. 2. TEAM: the CTA's warps share one
+// block (an instance of its own: the shares cost the others 4 %). Two stages per warp are in
 // flight: one more costs the L1 more than it hides (20 warps of 8 KB leave it 68 KB).
-template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
-    k_chunk_tc(const __grid_constant__ ChunkArgs a) {
+template <int D, bool E4M3, int NT, bool TEAM>
+__global__ void __launch_bounds__(kWarps * 32, 4) k_chunk_tc(const __grid_constant__ ChunkArgs a) {
   using Y = Stage<D, E4M3>;
   extern __shared__ __align__(1024) uint8_t s_stages[];
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int x = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5;
+  const int x = TEAM ? blockIdx.x : blockIdx.x * kWarps + warp;
   if (x >= a.blocks) return;
   const int h = blockIdx.y / a.groups, grp = blockIdx.y % a.groups, layer = blockIdx.z;
 
@@ -339,12 +335,22 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_stages) +
-                        (threadIdx.x >> 5) * (2 * Y::kBytes);
+                        warp * (2 * Y::kBytes);
   const int hrow = h * a.pd.d, page_rows = a.Hkv * a.pd.d;
+  // a team member's share: the last one has the offsets, the others every window_by-th
+  // pair of window tiles from the window_at-th on (0: none)
+  const bool offsets = !TEAM || warp == kWarps - 1;
+  const int window_by = !TEAM ? 1 : NT == 0 ? kWarps : offsets ? 0 : kWarps - 1;
+  const int window_at = TEAM && window_by ? warp : 0;
+  int n_far = a.n_off;                   // offsets that have rows of their own
+  unsigned near_lo = 0, near_hi = 0;     // distances 0..31 and 32..63 folded into the window
 
   auto run = [&](auto kind) {
-    constexpr bool FLAT = decltype(kind)::value;      // integer distances only
-    constexpr int STEP = FLAT ? 2 : 1;                // tokens of an offset stage
+    // 0: interpolated distances; integer ones: 1: 16 offsets a tile, 2: up to 8
+    // offsets left besides the folded ones, two tokens a tile
+    constexpr int KIND = decltype(kind)::value;
+    constexpr bool FLAT = KIND > 0;
+    constexpr int STEP = KIND == 2 ? 4 : KIND + 1;      // tokens of an offset stage
     auto find = [&](int r, int& left) {
       const int lp = quotient(a.pd, r), in = r - lp * a.pd.d;
       int page = __ldg(table + lp);
@@ -383,12 +389,14 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
 
     // Offset stages. Interpolated: one per (token, tile pair); tile i of the pair
     // has, for 8 offsets, rows a in 0..7 and rows b in 8..15. Integer distances: a
-    // tile holds 16 offsets of one token, a stage those of two tokens.
+    // tile holds 16 offsets of one token, or 8 of two.
     int lo_[NT > 0 ? NT : 1], c_[NT > 0 ? NT : 1];      // of the row this lane looks up
-    const int ahead = FLAT ? lane >> 4 : 0;             // for token t + ahead
+    const int ahead = KIND == 2 ? lane >> 3 : (KIND == 1 ? lane >> 4 : 0);      // for token t + ahead
 #pragma unroll
     for (int pair = 0; pair < NT; ++pair) {
-      const int src = pair * 16 + (FLAT ? lane & 15 : (lane >> 4) * 8 + (lane & 7));
+      const int src = pair * 16 + (KIND == 2   ? lane & 7
+                                   : KIND == 1 ? lane & 15
+                                               : (lane >> 4) * 8 + (lane & 7));
       const bool isb = !FLAT && (lane & 8);
       lo_[pair] = __shfl_sync(0xffffffffu, off_lo, src) + isb;
       c_[pair] = __shfl_sync(0xffffffffu, off_c, src);
@@ -407,15 +415,21 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
         if (w.left < 0) w.row = find(p - lo_[pair], w.left);
       }
       stage_in(keys ? kb : vb, there ? w.row : fill,
-               FLAT ? next_t + 1 < count : pair * 16 + 8 < a.n_off, keys);
+               FLAT ? next_t + STEP / 2 < count : pair * 16 + 8 < a.n_off, keys);
       if (pair == NT - 1) next_t += STEP;
     };
-    const int n_off = NT * ((count + STEP - 1) / STEP);
+    auto restart = [&]() {      // the values go over the same tokens again
+      next_t = 0;
+#pragma unroll
+      for (int pair = 0; pair < NT; ++pair) walk[pair] = Walk();
+    };
+    const int n_off = (KIND == 2 && n_far == 0) || !offsets ? 0 : NT * ((count + STEP - 1) / STEP);
 
     // Window tiles of 16 rows from `base`, the sinks as tile -1 before them.
     const int last = pos0 + count - 1;
     const int base = max(0, pos0 - (a.W - 1));
-    const int t_first = a.S > 0 ? -1 : 0, t_past = (last - base) / 16 + 1;
+    const int t_first = (a.S > 0 ? -1 : 0) + 2 * window_at, t_step = 2 * window_by;
+    const int t_past = !TEAM || window_by ? (last - base) / 16 + 1 : t_first;
     int win_row = 0, win_t = t_first;      // rows and first tile of the last key stage
     auto window_in = [&](int t0, bool keys) {
       if (keys) {
@@ -428,14 +442,26 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
       stage_in(keys ? kb : vb, win_row, win_t + 1 < t_past, keys);
     };
     // stage k of the whole order for k = 0 and 1, and from then on two ahead
-    if constexpr (NT == 0) {
-      window_in(t_first, true); commit();
-      window_in(t_first, false); commit();
-    } else {
-      offset_in(0, true); commit();
-      if (n_off > 1) offset_in(NT - 1, true); else window_in(t_first, true);
-      commit();
-    }
+    // (a team's member may have no offsets, or no window)
+    const int n_win = t_first < t_past ? 2 : 0;      // its first key and value stage
+    auto after_keys = [&](int k) {      // stage k >= n_off, for k up to n_off + 1
+      if (k < n_off + n_win)
+        window_in(t_first, k == n_off);
+      else if (NT > 0 && k - n_win < 2 * n_off) {
+        if (k - n_win == n_off) restart();
+        offset_in(NT == 2 ? (k - n_win - n_off) & 1 : 0, false);
+      }
+    };
+    if (NT > 0 && n_off > 0)
+      offset_in(0, true);
+    else
+      after_keys(0);
+    commit();
+    if (NT > 0 && n_off > 1)
+      offset_in(NT - 1, true);
+    else
+      after_keys(1);
+    commit();
 
     // Query fragments of column g. For e4m3 rows in fp16, times a power of two that
     // brings the column's largest element to [2^14, 2^15): an element loses bits
@@ -493,7 +519,22 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
     // times l. For e4m3 rows the reference is the maximum of score + log2(value
     // scale): the weights that go into P V, probability * value scale, are then at
     // most 1 and fit fp16 whatever the scales.
-    constexpr int NS = NT > 0 ? 2 * NT : 1;
+    constexpr int NS = NT > 0 && KIND != 2 ? 2 * NT : 1;
+    float beta[2] = {0.f, 0.f};
+    if (NT > 0 && a.beta) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (tok[e] >= 0)
+          beta[e] = kLog2e * __ldg(a.beta + ((size_t)layer * a.N + n0 + tok[e]) * a.Hq + head0 +
+                                   sub[e]);
+    }
+    // a folded offset is its window row a second time: log2(1 + 2^beta) more score
+    [[maybe_unused]] float extra[2] = {0.f, 0.f};
+    if (KIND == 2 && (near_lo | near_hi)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)      // (from the larger of the two terms)
+        extra[e] = fmaxf(beta[e], 0.f) + log2f(1.f + exp2f(-fabsf(beta[e])));
+    }
     [[maybe_unused]] float sig[NS][2], wg[NS];      // scores, and weights of row b, of offset 8 i + g
     if constexpr (NT > 0) {
       // ---- offset scores: a lane keeps its own columns' ----
@@ -504,10 +545,10 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
         sig[i][0] = sig[i][1] = vl[i][0] = vl[i][1] = 0.f;
       }
       int k = 2;      // the stage after the next
-      for (int t = 0; t < count; t += STEP) {
+      for (int t = 0; k < n_off + 2; t += STEP) {
 #pragma unroll
         for (int pair = 0; pair < NT; ++pair, ++k) {
-          const bool second = FLAT ? t + 1 < count : pair * 16 + 8 < a.n_off;
+          const bool second = FLAT ? t + STEP / 2 < count : pair * 16 + 8 < a.n_off;
           const uint32_t stage = take();
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -520,7 +561,19 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
               va = log_scale(row_scale(stage, 1, i, 0));
               vc = log_scale(row_scale(stage, 1, i, 1));
             }
-            if constexpr (FLAT) {      // rows g and g + 8: offsets 16 pair + g and + 8
+            if constexpr (KIND == 2) {      // rows g and g + 8: offset g of two tokens
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (tok[e] == t + 2 * i) {
+                  sig[0][e] = s[e] * ka;
+                  vl[0][e] = va;
+                }
+                if (tok[e] == t + 2 * i + 1) {
+                  sig[0][e] = s[2 + e] * kc;
+                  vl[0][e] = vc;
+                }
+              }
+            } else if constexpr (FLAT) {      // offsets 16 pair + g and 8 further
 #pragma unroll
               for (int e = 0; e < 2; ++e)
                 if (tok[e] == t + i) {
@@ -544,21 +597,14 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
           if (k < n_off)
             offset_in(pair, true);
           else
-            window_in(t_first, k == n_off);
+            after_keys(k);
           commit();
         }
       }
-      float beta[2] = {0.f, 0.f};
-      if (a.beta) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (tok[e] >= 0)
-            beta[e] = kLog2e * __ldg(a.beta + ((size_t)layer * a.N + n0 + tok[e]) * a.Hq + head0 +
-                                     sub[e]);
-      }
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        const int cc = __shfl_sync(0xffffffffu, off_c, i * 8 + g);
+        const int c_of = __shfl_sync(0xffffffffu, off_c, i * 8 + g);
+        const int cc = offsets ? c_of : 0x7fffffff;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           sig[i][e] = cc <= qpos[e] ? fmaf(sig[i][e], scale[e], beta[e]) : -INFINITY;
@@ -570,14 +616,11 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
         m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], d));
         m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], d));
       }
-      next_t = 0;
-#pragma unroll
-      for (int pair = 0; pair < NT; ++pair) walk[pair] = Walk();
     }
 
     // ---- window and sinks, two tiles of 16 rows at a time ----
-    for (int t0 = t_first; t0 < t_past; t0 += 2) {
-      const bool second = t0 + 1 < t_past, more = t0 + 2 < t_past;
+    for (int t0 = t_first; t0 < t_past; t0 += t_step) {
+      const bool second = t0 + 1 < t_past, more = t0 + t_step < t_past;
       float s[2][4], nm[2] = {-INFINITY, -INFINITY};
       uint32_t stage = take();
 #pragma unroll
@@ -605,15 +648,24 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
         for (int e = 0; e < 2; ++e) {
           s[i][e] = (unsigned)(qpos[e] - r0) < far ? s[i][e] * ka[e] : -INFINITY;
           s[i][2 + e] = (unsigned)(qpos[e] - r1) < far ? s[i][2 + e] * kc[e] : -INFINITY;
+          if (KIND == 2 && (near_lo | near_hi)) {      // (uniform)
+            const int l0 = qpos[e] - r0, l1 = qpos[e] - r1;
+            if (t >= 0 && (unsigned)l0 < 64u && ((l0 < 32 ? near_lo : near_hi) >> (l0 & 31) & 1u))
+              s[i][e] += extra[e];
+            if (t >= 0 && (unsigned)l1 < 64u && ((l1 < 32 ? near_lo : near_hi) >> (l1 & 31) & 1u))
+              s[i][2 + e] += extra[e];
+          }
           nm[e] = fmaxf(nm[e], E4M3 ? fmaxf(s[i][e] + va, s[i][2 + e] + vc)
                                     : fmaxf(s[i][e], s[i][2 + e]));
         }
       }
       __syncwarp();
       if (more)
-        window_in(t0 + 2, true);
-      else if (NT > 0)
+        window_in(t0 + t_step, true);
+      else if (NT > 0 && n_off > 0) {
+        restart();
         offset_in(0, false);
+      }
       commit();
 #pragma unroll
       for (int d = 4; d <= 16; d <<= 1) {
@@ -652,8 +704,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
       }
       __syncwarp();
       if (more)
-        window_in(t0 + 2, false);
-      else if (n_off > 1)
+        window_in(t0 + t_step, false);
+      else if (NT > 0 && n_off > 1)
         offset_in(NT - 1, false);
       commit();
     }
@@ -678,26 +730,30 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
         }
       }
       int k = 2;
-      for (int t = 0; t < count; t += STEP) {
+      for (int t = 0; k < n_off + 2; t += STEP) {
 #pragma unroll
         for (int pair = 0; pair < NT; ++pair, ++k) {
-          const bool second = FLAT ? t + 1 < count : pair * 16 + 8 < a.n_off;
+          const bool second = FLAT ? t + STEP / 2 < count : pair * 16 + 8 < a.n_off;
           const uint32_t stage = take();
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (i == 1 && !second) continue;
-            const int at = FLAT ? t + i : t;
-            const int ia = FLAT ? 2 * pair : 2 * pair + i, ib = FLAT ? 2 * pair + 1 : ia;
+            // tokens and offsets of rows 0..7 and 8..15
+            const int at = KIND == 2 ? t + 2 * i : (FLAT ? t + i : t);
+            const int bt = KIND == 2 ? at + 1 : at;
+            const int ia = KIND == 2 ? 0 : (FLAT ? 2 * pair : 2 * pair + i);
+            const int ib = KIND == 1 ? 2 * pair + 1 : ia;
             uint32_t p0, p1;
             if constexpr (E4M3) {
               const float wb = FLAT ? 1.f : wg[ia], wa = FLAT ? 1.f : 1.f - wb;
               const float va = row_scale(stage, 1, i, 0) * wa, vc = row_scale(stage, 1, i, 1) * wb;
-              const bool on0 = tok[0] == at, on1 = tok[1] == at;
-              p0 = transpose8(pack16<true>(on0 ? sig[ia][0] * va : 0.f, on1 ? sig[ia][1] * va : 0.f));
-              p1 = transpose8(pack16<true>(on0 ? sig[ib][0] * vc : 0.f, on1 ? sig[ib][1] * vc : 0.f));
+              p0 = transpose8(pack16<true>(tok[0] == at ? sig[ia][0] * va : 0.f,
+                                           tok[1] == at ? sig[ia][1] * va : 0.f));
+              p1 = transpose8(pack16<true>(tok[0] == bt ? sig[ib][0] * vc : 0.f,
+                                           tok[1] == bt ? sig[ib][1] * vc : 0.f));
             } else {
               p0 = tok_g == at ? pa[ia] : 0u;
-              p1 = tok_g == at ? (FLAT ? pa[ib] : pb[ib]) : 0u;
+              p1 = tok_g == bt ? (FLAT ? pa[ib] : pb[ib]) : 0u;
             }
             Y::add(stage, i, at_v, p0, p1, o);
           }
@@ -709,12 +765,87 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
     }
   };
   if (ok) {
-    if (NT > 0 && !__all_sync(0xffffffffu, off_w == 0.f))
-      run(std::false_type());
-    else
-      run(std::true_type());
+    if (NT == 0) {
+      run(std::integral_constant<int, 1>());
+    } else if (!__all_sync(0xffffffffu, off_w == 0.f)) {
+      run(std::integral_constant<int, 0>());
+    } else {
+      // Integer distances: an offset inside the window is a window row a second time.
+      // Such offsets (the first of each distance) are folded into the window's scores
+      // where that leaves at most 8 others, which then go two tokens to a tile.
+      if constexpr (NT == 1) {
+        const bool listed = lane < a.n_off;
+        const unsigned same = __match_any_sync(0xffffffffu, listed ? off_lo : -1 - lane);
+        const bool near = listed && off_lo < min(a.W, 64) && __ffs(same) == lane + 1;
+        unsigned far = __ballot_sync(0xffffffffu, listed && !near);
+        if (!TEAM && count > 2 && (far == 0 || (a.n_off > 8 && __popc(far) <= 8))) {
+          near_lo = __reduce_or_sync(0xffffffffu, near && off_lo < 32 ? 1u << off_lo : 0u);
+          near_hi = __reduce_or_sync(0xffffffffu, near && off_lo >= 32 ? 1u << (off_lo & 31) : 0u);
+        } else {
+          far = __ballot_sync(0xffffffffu, listed);
+        }
+        n_far = __popc(far);
+        if (n_far <= 8) {      // the others, in order, to lanes 0 .. n_far - 1
+          int* list = reinterpret_cast<int*>(s_stages + warp * (2 * Y::kBytes));
+          if (far >> lane & 1u) list[__popc(far & ((1u << lane) - 1u))] = off_lo;
+          __syncwarp();
+          off_lo = lane < n_far ? list[lane] : 0;
+          off_c = lane < n_far ? off_lo : 0x7fffffff;
+          __syncwarp();
+        }
+      }
+      if constexpr (NT == 1) {
+        if (n_far <= 8)
+          run(std::integral_constant<int, 2>());
+        else
+          run(std::integral_constant<int, 1>());
+      } else {
+        run(std::integral_constant<int, 1>());
+      }
+    }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  if constexpr (TEAM) {      // the first member joins the parts
+    constexpr int kPart = D / 4 + 4;      // floats of a lane's part
+    static_assert(kPart * 32 * 4 <= 2 * Y::kBytes, "a part fits a warp's stages");
+    float* mine = reinterpret_cast<float*>(s_stages + warp * (2 * Y::kBytes)) + lane;
+    __syncwarp();
+    if (warp > 0) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mine[(4 * j + e) * 32] = o[j][e];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mine[(D / 4 + e) * 32] = m[e];
+        mine[(D / 4 + 2 + e) * 32] = l[e];
+      }
+      if (__any_sync(0xffffffffu, lost) && lane == 0) {
+        mine[(D / 4) * 32] = __int_as_float(0x7fc00000);      // tells the first member
+        atomicOr(&g_chunk_err, kErrPage);
+      }
+    }
+    __syncthreads();      // (the returns before are the same for the whole CTA)
+    if (warp > 0) return;
+    for (int w = 1; w < kWarps; ++w) {
+      const float* part = reinterpret_cast<const float*>(s_stages + w * (2 * Y::kBytes)) +
+                          lane;
+      lost = lost || __shfl_sync(0xffffffffu, part[(D / 4) * 32] != part[(D / 4) * 32], 0);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mp = part[(D / 4 + e) * 32], top = fmaxf(m[e], mp);
+        const float z = top == -INFINITY ? 0.f : top;
+        const float f = exp2_approx(m[e] - z), fp = exp2_approx(mp - z);
+        m[e] = top;
+        l[e] = l[e] * f + part[(D / 4 + 2 + e) * 32] * fp;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          o[j][e] = o[j][e] * f + part[(4 * j + e) * 32] * fp;
+          o[j][2 + e] = o[j][2 + e] * f + part[(4 * j + 2 + e) * 32] * fp;
+        }
+      }
+    }
+  }
 #pragma unroll
   for (int d = 4; d <= 16; d <<= 1) {
     l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
@@ -745,7 +876,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 ? MB128 : MB64)
   // Outputs through shared memory: one row per column, 16 bytes apart in banks,
   // then 16 bytes a lane of consecutive head dims.
   constexpr int kOut = D * 2 + 16;
-  uint8_t* out = s_stages + (threadIdx.x >> 5) * (2 * Y::kBytes);
+  uint8_t* out = s_stages + warp * (2 * Y::kBytes);
   static_assert(8 * kOut <= 2 * Y::kBytes, "the output tile fits the stages");
   __syncwarp();
   const float bad = __int_as_float(0x7fc00000);
@@ -981,16 +1112,22 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const __grid_constant
   one_query<float, D, E4M3>(a, blockIdx.z, blockIdx.y, n, b, inside ? (int)posl : 0, inside);
 }
 
-template <int D, bool E4M3, int NT>
-cudaError_t launch_tc(const ChunkArgs& a, const dim3& grid, cudaStream_t st) {
+template <int D, bool E4M3, int NT, bool TEAM>
+cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t st) {
+  const dim3 grid(TEAM ? a.blocks : (a.blocks + kWarps - 1) / kWarps, a.Hkv * a.groups, a.L);
   constexpr int smem = kWarps * 2 * Stage<D, E4M3>::kBytes;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
-        k_chunk_tc<D, E4M3, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        k_chunk_tc<D, E4M3, NT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  k_chunk_tc<D, E4M3, NT><<<grid, kWarps * 32, smem, st>>>(a);
+  k_chunk_tc<D, E4M3, NT, TEAM><<<grid, kWarps * 32, smem, st>>>(a);
   return cudaSuccess;
+}
+
+template <int D, bool E4M3, int NT>
+cudaError_t launch_nt(const ChunkArgs& a, cudaStream_t st) {
+  return a.team ? launch_tc<D, E4M3, NT, true>(a, st) : launch_tc<D, E4M3, NT, false>(a, st);
 }
 
 template <int D, bool E4M3>
@@ -1001,10 +1138,9 @@ cudaError_t launch_t(const ChunkArgs& a, bool f32, cudaStream_t st) {
     const dim3 grid((a.N + kWarps - 1) / kWarps, a.Hq, a.L);
     k_chunk_f32<D, E4M3><<<grid, kWarps * 32, 0, st>>>(a);
   } else {
-    const dim3 grid((a.blocks + kWarps - 1) / kWarps, a.Hkv * a.groups, a.L);
-    e = a.n_off == 0 ? launch_tc<D, E4M3, 0>(a, grid, st)
-        : a.n_off <= 16 ? launch_tc<D, E4M3, 1>(a, grid, st)
-                        : launch_tc<D, E4M3, 2>(a, grid, st);
+    e = a.n_off == 0    ? launch_nt<D, E4M3, 0>(a, st)
+        : a.n_off <= 16 ? launch_nt<D, E4M3, 1>(a, st)
+                        : launch_nt<D, E4M3, 2>(a, st);
   }
   trace_mark("chunk_attn", st, false);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -1033,6 +1169,13 @@ cudaError_t launch_chunk_attn(const PagedProblem& p, const PagedPtrs& c, const C
   a.inv_per = (256 + a.per - 1) / a.per;
   a.shift = a.per == 1 ? 3 : (a.per == 2 ? 2 : (a.per <= 4 ? 1 : 0));
   a.blocks = a.shift ? (p.N >> a.shift) + p.B : p.N;
+  const long long warps = (long long)a.blocks * a.Hkv * a.groups * a.L;
+  const long long rows = (long long)x.W + (1 << a.shift) - 1;
+  // Few blocks, as in a decode step, and a window of three tiles or more (the sinks
+  // are one): a CTA's warps share a block while all CTAs are resident at once, four
+  // per SM (one token, 16 heads, window 64 with sinks: 8.9 -> 6.9 us; with a window
+  // of one pair of tiles the join costs what it saves).
+  a.team = (rows + 15) / 16 + (x.S > 0) >= 3 && warps <= 148 * 4;
   const bool f32 = p.dtype == SA_DTYPE_F32, q8 = p.format == SA_CACHE_E4M3;
   switch (p.D) {
     case 16: return q8 ? launch_t<16, true>(a, f32, st) : launch_t<16, false>(a, f32, st);

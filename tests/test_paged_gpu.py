@@ -87,6 +87,18 @@ CHUNK = [
 ]
 
 
+# Integer distances, in and out of the window, twice the same, at its edge, at 0, all of them in
+# it, more than 8 outside; and rows enough for several key tiles
+for n, (offs, alphas, W) in enumerate([
+        ((1, 2, 3), [1.0, 2.0], 12), ((5, 5, 1, 12, 11, 13, 5), [1.0], 12), (FIB, [1.0, 2.0], 22),
+        (FIB, [3.0, 0.0], 64), ((63, 64, 65, 1, 31, 32, 33, 90, 2, 3), [1.0], 80),
+        (tuple(range(1, 17)), [1.0, 4.0], 8), (tuple(range(1, 17)), [1.0], 100)]):
+    for dtype, fmt, D, Hq, Hkv in ((BF, "plain", 64, 2, 2), (BF, "e4m3", 32, 4, 1),
+                                   (BF, "plain", 16, 6, 2), (F32, "plain", 16, 1, 1)):
+        CHUNK.append((f"integer_{n}_{fmt}_{Hq}x{D}", dtype, fmt, D, Hq, Hkv, 16, W, n % 3, offs, alphas,
+                      [0, 130, 9], [21, 1, 14], 0, 0))
+
+
 @pytest.mark.parametrize("prior", [False, True], ids=["", "prior"])
 @pytest.mark.parametrize("case", CHUNK, ids=[c[0] for c in CHUNK])
 def test_chunk_matches_the_plain_form(case, prior):
@@ -525,3 +537,22 @@ def test_a_long_cache_past_32_bit_offsets():
     k2, v2 = sa.cache_read(small, t2, i32([70]))
     for a, b in ((q, q2), (o, o2), (lse, lse2), (k, k2), (v, v2)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("W,S,offs", [(12, 0, FIB), (64, 4, FIB), (200, 16, (3, 77)), (500, 0, ()),
+                                      (1, 0, (1,)), (20, 1, MANY)])
+@pytest.mark.parametrize("dtype,fmt,D,Hq,Hkv,B", [
+    (BF, "plain", 64, 2, 2, 3), (BF, "e4m3", 128, 8, 2, 2), (BF, "plain", 16, 1, 1, 1),
+    (BF, "e4m3", 16, 20, 2, 2), (BF, "plain", 128, 3, 1, 40), (F32, "plain", 64, 2, 1, 2)])
+def test_single_tokens(dtype, fmt, D, Hq, Hkv, B, W, S, offs):
+    """Decode steps: the smallest calls, whose blocks are shared by several warps, and one of
+    more blocks than that."""
+    alpha = [1.0, 0.9]
+    old = [(37 * b * b + 450 * (b % 2)) % 701 for b in range(B)]
+    t = plain.Batch(2, Hkv, D, 16, old, [1] * B, dtype, fmt, seed=W + S)
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn((2, t.N, Hq, D), generator=g).to(dtype)
+    beta = torch.randn((2, t.N, Hq), generator=g)
+    out, lse = _run_chunk(t, q.to(DEV), alpha, window=W, sinks=S, offsets=offs, beta=beta)
+    ref = plain.chunk(q.double(), t.keys, t.vals, t.cu, t.old, alpha, W, S, offs, beta=beta.double())
+    _check_chunk(t, q, out, lse, ref, dtype, min(W, max(t.held)) + S + 2 * len(offs))
