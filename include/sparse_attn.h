@@ -307,8 +307,8 @@ sa_status sparse_attn_qk_norm_rope_bwd(const sa_qk_norm_params* p, const void* q
  * (cu_q: device int32 [B+1], not decreasing, cu_q[0] >= 0), at positions
  * cached[b], cached[b]+1, ... (cached: device int32 [B], the rows that the
  * sequence holds before). A sequence may have none. Rows that belong to no
- * sequence (below cu_q[0], or from cu_q[B] on) are padding: nothing is read for
- * them and their outputs stay as they were. cu_q, cached and page_table are read
+ * sequence (below cu_q[0], or from cu_q[B] on) are padding: their values do not
+ * matter and their outputs stay as they were. cu_q, cached and page_table are read
  * on the device, so a captured graph follows their contents; a page index
  * outside [0, n_pages), or a position outside [0, max_pages * page_size), sets
  * bit 3 of the device error word and no such row is touched: appends skip the

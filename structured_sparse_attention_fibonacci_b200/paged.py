@@ -148,16 +148,21 @@ def _output(name, out, like, others):
     return out
 
 
+def _overlap(a, b):
+    a0, a1 = _span(a)
+    b0, b1 = _span(b)
+    return a0 < b1 and b0 < a1
+
+
 def _apart(name, out, own, others):
     """out is `own` (contiguous) or shares no memory with it, and none with others."""
     if not out.numel():
         return
-    a0, a1 = _span(out)
-    for o in (own, *others):
-        if o is None or not o.numel():
-            continue
-        b0, b1 = _span(o)
-        if a0 < b1 and b0 < a1 and not (o is own and a0 == b0 and o.is_contiguous()):
+    if own is not None and own.numel() and _overlap(out, own):
+        if out.data_ptr() != own.data_ptr() or not own.is_contiguous():
+            raise ValueError(f"{name} overlaps its input")
+    for o in others:
+        if o is not None and o.numel() and _overlap(out, o):
             raise ValueError(f"{name} overlaps another tensor of the call")
 
 
@@ -294,8 +299,8 @@ def cache_append(q, k, v, cache, page_table, cu_q, cached, *, q_weight=None, k_w
 
     q [L, N, Hq, D], k and v [L, N, Hkv, D]: bf16 or fp32 with contiguous rows,
     otherwise of any strides.  Rows cu_q[b] .. cu_q[b + 1] - 1 are sequence b's new
-    tokens, at positions cached[b], cached[b] + 1, ...; other rows are padding and
-    their q_out stays as it was.  Row r of a sequence lies in slot r % page_size of
+    tokens, at positions cached[b], cached[b] + 1, ...; other rows are padding,
+    whose values do not matter and whose q_out stays as it was.  Row r of a sequence lies in slot r % page_size of
     page page_table[b, r // page_size].  cu_q [B + 1], cached [B] and page_table
     [B, max_pages] are int32 and read on the device.  No two sequences with new
     tokens may share the pages that are written."""

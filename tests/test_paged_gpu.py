@@ -556,3 +556,74 @@ def test_single_tokens(dtype, fmt, D, Hq, Hkv, B, W, S, offs):
     out, lse = _run_chunk(t, q.to(DEV), alpha, window=W, sinks=S, offsets=offs, beta=beta)
     ref = plain.chunk(q.double(), t.keys, t.vals, t.cu, t.old, alpha, W, S, offs, beta=beta.double())
     _check_chunk(t, q, out, lse, ref, dtype, min(W, max(t.held)) + S + 2 * len(offs))
+
+
+def test_many_sequences_and_shared_pages():
+    """1100 sequences with none to two new tokens; all of them read one sequence's first two pages
+    as their own (a shared prompt), the rest lies in a page of their own."""
+    B, page, D = 1100, 16, 32
+    new = [(b * 7) % 3 for b in range(B)]
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    g = torch.Generator().manual_seed(0)
+    kp, vp = (torch.randn((1, B + 2, 1, page, D), generator=g).to(BF) for _ in range(2))
+    table = torch.stack([torch.full((B,), B), torch.full((B,), B + 1), torch.randperm(B, generator=g)],
+                        1).to(torch.int32)
+    old = [32 + b % 13 for b in range(B)]
+    q = torch.randn((1, cu[-1], 2, D), generator=g).to(BF)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    alpha = [0.75]
+    o, lse = sa.chunk_attn(q.to(DEV), sa.PagedCache(kp.to(DEV), vp.to(DEV)), table.to(DEV), i32(cu),
+                           i32(old), torch.tensor(alpha, device=DEV), window=10, sinks=2)
+    seqs = [[x[:, t.long()].transpose(1, 2).flatten(2, 3).double() for t in table] for x in (kp, vp)]
+    ro, rl, mag, big = plain.chunk(q.double(), *seqs, cu, old, alpha, 10, 2, FIB)
+    assert ((lse.cpu().double() - rl).abs() <= 2.0 ** -20 * (big + rl.abs() + 1)).all()
+    tol = (2.0 ** -18 * (big[..., None] + 1) + 2.0 ** -19 + 2.0 ** -8) * mag + 2.0 ** -8 * ro.abs()
+    assert ((o.cpu().double() - ro).abs() <= tol).all()
+    # and without the sums
+    o2, none = sa.chunk_attn(q.to(DEV), sa.PagedCache(kp.to(DEV), vp.to(DEV)), table.to(DEV), i32(cu),
+                             i32(old), torch.tensor(alpha, device=DEV), window=10, sinks=2,
+                             want_lse=False)
+    assert none is None and torch.equal(o, o2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("qscale", [1.0, 1e-12, 1e9])
+def test_scales_and_queries_of_any_size(dtype, qscale):
+    """8-bit rows with scales that no append writes: not powers of two, zero, negative, from 1e-30
+    to 1e10 side by side; queries of any size against keys that keep the scores moderate."""
+    t = plain.Batch(1, 1, 64, 16, [40, 0], [30, 9], dtype, "e4m3", seed=12)
+    g = torch.Generator().manual_seed(4)
+    vs = torch.randn(t.vs.shape, generator=g) * 10.0 ** torch.randint(-30, 11, t.vs.shape, generator=g)
+    vs = torch.where(torch.rand(t.vs.shape, generator=g) < 0.1, torch.zeros(()), vs)
+    ks = torch.rand(t.ks.shape, generator=g) * 0.02 / qscale
+    t.ks, t.vs = ks, vs
+    for b in range(2):
+        for r in range(t.held[b]):
+            at = (slice(None), int(t.table[b, r // 16]), slice(None), r % 16)
+            t.keys[b][:, :, r] = t.k[at].double() * ks[at].double()[..., None]
+            t.vals[b][:, :, r] = t.v[at].double() * vs[at].double()[..., None]
+    q = (torch.randn((1, t.N, 1, 64), generator=g) * qscale).to(dtype)
+    alpha = [1.3]
+    out, lse = _run_chunk(t, q.to(DEV), alpha, window=12)
+    ref = plain.chunk(q.double(), t.keys, t.vals, t.cu, t.old, alpha, 12, 0, FIB)
+    _check_chunk(t, q, out, lse, ref, dtype, 27)
+
+
+@pytest.mark.parametrize("dtype,fmt", [(BF, "plain"), (BF, "e4m3"), (F32, "plain")])
+def test_a_query_of_nan_or_infinities_stays_alone(dtype, fmt):
+    t = plain.Batch(1, 1, 64, 16, [30], [16], dtype, fmt, seed=13)
+    q = torch.randn((1, 16, 2, 64), generator=torch.Generator().manual_seed(6)).to(dtype)
+    good, _ = _run_chunk(t, q.to(DEV), [1.0], window=20)
+    q2 = q.clone()
+    q2[0, 3, 1, 5] = math.nan
+    q2[0, 9, 0, 7] = math.inf
+    out, lse = _run_chunk(t, q2.to(DEV), [1.0], window=20)
+    spoiled = torch.zeros((16, 2), dtype=torch.bool)
+    spoiled[3, 1] = spoiled[9, 0] = True
+    assert torch.isnan(out[0][spoiled].float()).all() and torch.isnan(lse[0][spoiled]).all()
+    # (a block with such a query is computed query by query: both results are within 2^-8 (A + |O|)
+    # of the exact one, for |O| <= A <= 3)
+    assert ((out[0][~spoiled].float() - good[0][~spoiled].float()).abs() <= 0.05).all()
+    assert torch.isfinite(lse[0][~spoiled]).all()

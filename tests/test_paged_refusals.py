@@ -185,6 +185,8 @@ def test_binding_refuses_tensors_that_do_not_fit():
     with pytest.raises(ValueError):      # an output that overlaps its input, shifted
         sa.qk_norm_rope(big.view(-1)[64:64 + q.numel()].view(q.shape), k, w, w,
                         q_out=big.view(-1)[:q.numel()].view(q.shape))
+    with pytest.raises(ValueError):      # one tensor for both outputs
+        sa.qk_norm_rope(q, q, w, w, q_out=q, k_out=q)
     with pytest.raises(ValueError):
         sa.qk_norm_rope_bwd(q, k, w, w, q, k[:, :, :1])
     with pytest.raises(sa.SparseAttnError):
