@@ -1,1152 +1,8 @@
-// Attention of a chunk of new tokens over the paged cache: for every layer,
-// token row n of sequence b (position pos = cached[b] + n - cu_q[b], its own
-// row already in the cache) and query head, the members of row pos of the
-// forward ("Depth-Staggered Fibonacci Spacing for Sparse Attention",
-// Methodology: attended set, scaling, interpolation):
-//   window rows pos-W+1 .. pos, sinks j < S with j <= pos, and per offset f
-//   (1-w) row[pos-lo] + w row[pos-lo-1],  d = alpha f, lo = floor(d), w = d-lo,
-//   while pos - ceil(d) >= 0;
-//   s = scale q . k (+ beta on the offset members);  o = softmax(s) v.
-// Keys are rotated in the cache and the queries by cache_append.
-//
-// 16-bit queries (k_chunk_tc): products on the tensor cores by mma.sync
-// m16n8k16, one warp per block of 8 columns. A column is a (token, query head)
-// pair that shares one key/value head: with G heads per key/value head a block
-// holds 8/G consecutive tokens. Scores are S^T = K q^T (M = 16 gathered rows,
-// N = 8 columns) and outputs O^T = V^T P^T (M = 16 head dims, N = 8 columns), so
-// that eight columns, not sixteen, have to be filled. Gathered rows go straight
-// from global memory into A fragments: the contraction index of a product may be
-// permuted, so a lane takes 16 contiguous bytes of its row (and the query
-// fragments the same), and a pair of V rows becomes a fragment by byte
-// permutes. Nothing is staged, no barrier is needed, and a row read by several
-// tokens is an L1 hit. tcgen05 has no form for this gather: its A operand is a
-// tile of 128 rows in tensor or shared memory, of which a token's 15 interpolated
-// pairs would fill a quarter, after a copy through shared memory.
-//   - Window and sinks: tiles of 16 rows shared by all columns, masked, with a
-//     running maximum and sum per column.
-//   - Offsets: for each token tiles of 8 offsets, row a of offset g in row g of
-//     the tile and row b in row g + 8, so that one lane holds both dot products
-//     and interpolates in registers. Only the token's own columns of such a
-//     tile count: over the block's tokens a lane keeps just its own two
-//     columns, 2 scores per tile in all.
-// Rounding: products of 16-bit (or e4m3) values are exact, sums fp32; the
-// probabilities are rounded to bf16 for P V (2^-9 each, below the output's own
-// rounding on average), their sum is not. e4m3 codes are used as bf16 values, the
-// row scales (powers of two) multiply the scores and the probabilities.
-// A masked probability is 0, and 0 * Inf or NaN is NaN: when a block of several
-// tokens ends with a non-finite output, its tokens are computed again one by
-// one, where no masked row is loaded at all.
-//
-// 32-bit queries (k_chunk_f32): one warp per (token, query head) on the CUDA
-// cores, chunks of 32 members: four lanes per member for the scores, lanes over
-// head dims for the values.
-#include <type_traits>
-
-#include "sa_paged.cuh"
+// Attention of a chunk of new tokens over the paged cache: choice of the kernel
+// instance. The kernels are in sa_chunk.cuh.
+#include "sa_chunk.cuh"
 
 namespace sa {
-
-namespace {
-
-__device__ unsigned g_chunk_err;
-
-constexpr int kWarps = 4;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct ChunkArgs {
-  int L, N, B, Hq, Hkv, n_pages, max_pages, W, n_off, S, blocks;
-  int G, groups, per, shift;      // heads per kv head; column groups, heads in one, log2 tokens
-  bool team;                      // a CTA's warps share a block
-  int inv_per;                    // ceil(256 / per): col * inv_per / 256 = col / per for col < 8
-  FastDiv pd;
-  float scale;
-  int f[SA_MAX_OFFSETS];
-  int64_t ql, qn, qh;
-  const void* q; const void* kc; const void* vc; const float* ks; const float* vs;
-  const float* alpha; const float* beta;
-  const int* table; const int* cu; const int* cached;
-  void* o; float* lse;
-};
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// One m16n8k16 product with fp32 sums, of bf16 (plain rows) or fp16 (e4m3 rows,
-// whose codes are exact in fp16) operands.
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (F16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-template <bool F16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-  if constexpr (F16) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    return pack_bf16x2(lo, hi);
-  }
-}
-
-// Transpose of an 8x8 matrix of 16-bit values (lane (g, c) holds row g, columns
-// 2c and 2c+1).
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
-template <int BYTES>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
-  if constexpr (BYTES == 16) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-  } else if constexpr (BYTES == 8) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    w[0] = u.x; w[1] = u.y;
-  } else if constexpr (BYTES == 4) {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  } else {
-    static_assert(BYTES == 2, "unsupported width");
-    w[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
-  }
-}
-
-// Four e4m3 codes as two pairs of fp16 values: exact, NaN kept.
-__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; "
-      "cvt.rn.f16x2.e4m3x2 %1, b; }"
-      : "=r"(lo), "=r"(hi)
-      : "r"(four));
-}
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-template <bool TRANS, int OFFSET>
-__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
-  if constexpr (TRANS)
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4 + %5];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr), "n"(OFFSET)
-                 : "memory");
-  else
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4 + %5];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr), "n"(OFFSET)
-                 : "memory");
-}
-__device__ __forceinline__ float load_shared(uint32_t addr) {
-  float x;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
-  return x;
-}
-
-// A stage: 32 gathered rows (two tiles of 16) of K or V, in 16-byte chunks whose
-// place is exchanged by row (so that eight rows of one chunk column, an ldmatrix
-// phase, fall into different banks), and for e4m3 rows their scales.
-template <int D, bool E4M3>
-struct Stage {
-  static constexpr int kRow = D * (E4M3 ? 1 : 2);       // bytes
-  static constexpr int kChunks = kRow / 16;
-  static constexpr int kTile = 16 * kRow;
-  static constexpr int kScales = 2 * kTile;             // offset of the key scales, then the values'
-  static constexpr int kBytes = 2 * kTile + (E4M3 ? 256 : 0);
-  static __device__ __forceinline__ int place(int row, int chunk) {
-    constexpr int kPer = kChunks >= 8 ? 1 : 8 / kChunks;
-    constexpr int kMask = kChunks >= 8 ? 7 : kChunks - 1;
-    return row * kRow + ((chunk ^ ((row / kPer) & kMask)) << 4);
-  }
-  // Copies the rows that the lanes name (pool rows; lane = row of the stage). Of
-  // its place a lane keeps the part that does not depend on the pass (own = place
-  // of its chunk in pass 0); `pool` points at its chunk of row 0.
-  static __device__ __forceinline__ int own() {
-    const int lane = threadIdx.x & 31;
-    return place(lane / kChunks, lane % kChunks);
-  }
-  static __device__ __forceinline__ void fill(uint32_t stage, int own, const uint8_t* pool,
-                                              int row, bool two) {
-    constexpr int kRows = 32 / kChunks;      // rows of a pass
-    const int r0 = (threadIdx.x & 31) / kChunks;
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      if (i == kChunks / 2 && kChunks > 1 && !two) break;
-      constexpr int kMask = kChunks >= 8 ? 7 : 0;      // passes of fewer than 8 rows
-      const int turn = ((i * kRows) & kMask) << 4;
-      const int r = __shfl_sync(0xffffffffu, row, i * kRows + r0);
-      copy16(stage + (own ^ turn) + i * kRows * kRow, pool + (int64_t)r * kRow);
-    }
-  }
-  // Lane offset of an ldmatrix of K (matrices: row halves, then chunks) or V
-  // (chunks, then row halves); step s of the loop over chunk pairs is at ^ (s << 5).
-  static __device__ __forceinline__ uint32_t lane_at(bool v) {
-    const int lane = threadIdx.x & 31, mi = lane >> 3;
-    const int half = v ? mi >> 1 : mi & 1, chunk = v ? mi & 1 : mi >> 1;
-    return place((lane & 7) + 8 * half, kChunks > 1 ? chunk : 0);
-  }
-  // S^T of a tile's 16 keys with the block's 8 columns.
-  static __device__ __forceinline__ void scores(uint32_t stage, int tile, uint32_t at,
-                                                const uint32_t (&q)[D / 8], float (&s)[4]) {
-    s[0] = s[1] = s[2] = s[3] = 0.f;
-    if constexpr (!E4M3) {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {      // 16 elements: two chunks
-        uint32_t r[4];
-        tile == 0 ? ldmatrix4<false, 0>(stage + (at ^ (i << 5)), r)
-                  : ldmatrix4<false, kTile>(stage + (at ^ (i << 5)), r);
-        mma16816<false>(s, r[0], r[1], r[2], r[3], q[2 * i], q[2 * i + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < (kChunks + 1) / 2; ++i) {      // 16 codes a chunk, two chunks
-        uint32_t r[4];
-        tile == 0 ? ldmatrix4<false, 0>(stage + (at ^ (i << 5)), r)
-                  : ldmatrix4<false, kTile>(stage + (at ^ (i << 5)), r);
-#pragma unroll
-        for (int j = 0; j < (kChunks > 1 ? 2 : 1); ++j) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x4(r[2 * j], a0, a2);
-          e4m3x4_to_f16x4(r[2 * j + 1], a1, a3);
-          mma16816<true>(s, a0, a1, a2, a3, q[4 * i + 2 * j], q[4 * i + 2 * j + 1]);
-        }
-      }
-    }
-  }
-  // O^T += V^T P^T of a tile's 16 values; p0, p1: P^T for rows 0..7 and 8..15.
-  // Lane g's head dims of product j: 16 j + g and 16 j + 8 + g, for e4m3 rows
-  // 16 j + 2 g and the next.
-  static __device__ __forceinline__ void add(uint32_t stage, int tile, uint32_t at, uint32_t p0,
-                                             uint32_t p1, float (&o)[D / 16][4]) {
-    if constexpr (!E4M3) {
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        uint32_t r[4];
-        tile == 0 ? ldmatrix4<true, 0>(stage + (at ^ (j << 5)), r)
-                  : ldmatrix4<true, kTile>(stage + (at ^ (j << 5)), r);
-        mma16816<false>(o[j], r[0], r[1], r[2], r[3], p0, p1);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < (kChunks + 1) / 2; ++i) {
-        uint32_t r[4];
-        tile == 0 ? ldmatrix4<true, 0>(stage + (at ^ (i << 5)), r)
-                  : ldmatrix4<true, kTile>(stage + (at ^ (i << 5)), r);
-#pragma unroll
-        for (int j = 0; j < (kChunks > 1 ? 2 : 1); ++j) {
-          // two rows of a pair of codes to two pairs of rows of a code
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x4(__byte_perm(r[j], 0, 0x3120), a0, a1);
-          e4m3x4_to_f16x4(__byte_perm(r[2 + j], 0, 0x3120), a2, a3);
-          mma16816<true>(o[2 * i + j], a0, a1, a2, a3, p0, p1);
-        }
-      }
-    }
-  }
-};
-
-template <typename QT, int D, bool E4M3>
-__device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, int n, int b,
-                                       int pos, bool inside);
-
-// A lane's walk over the pool rows that one member has for consecutive tokens:
-// mostly the next row of the same page.
-struct Walk {
-  int row = 0, left = -1;      // the last row, and how many follow it in its page
-};
-
-// ---------------------------------------------------------------------------
-// NT: pairs of offset tiles (16 offsets each), 0 .. 2. TEAM: the CTA's warps share one
-// block (an instance of its own: the shares cost the others 4 %). Two stages per warp are in
-// flight: one more costs the L1 more than it hides (20 warps of 8 KB leave it 68 KB).
-template <int D, bool E4M3, int NT, bool TEAM>
-__global__ void __launch_bounds__(kWarps * 32, 4) k_chunk_tc(const __grid_constant__ ChunkArgs a) {
-  using Y = Stage<D, E4M3>;
-  extern __shared__ __align__(1024) uint8_t s_stages[];
-  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int warp = threadIdx.x >> 5;
-  const int x = TEAM ? blockIdx.x : blockIdx.x * kWarps + warp;
-  if (x >= a.blocks) return;
-  const int h = blockIdx.y / a.groups, grp = blockIdx.y % a.groups, layer = blockIdx.z;
-
-  // this block's tokens: rows n0 .. n0 + count - 1, positions from pos0
-  const int b = find_sequence(a.cu, a.B, a.shift, x);
-  const int first = __ldg(a.cu + b), past = min(__ldg(a.cu + b + 1), a.N);
-  const long long n0l = (long long)first + ((long long)(x - (first >> a.shift) -
-                                                        (a.shift ? b : 0)) << a.shift);
-  if (first < 0 || n0l < first || n0l >= past) return;
-  const int n0 = (int)n0l, count = min(1 << a.shift, past - n0);
-  const long long posl = (long long)__ldg(a.cached + b) + (n0 - first);
-  const bool inside = posl >= 0 && posl + count <= (long long)a.max_pages * a.pd.d;
-  const int pos0 = inside ? (int)posl : 0;
-
-  // offset geometry: lane k holds offset k
-  int off_lo = 0, off_c = 0x7fffffff;
-  float off_w = 0.f;
-  bool ok = inside;
-  if (NT > 0 && lane < a.n_off) {
-    const OffGeo og = offset_geometry(__ldg(a.alpha + layer), a.f[lane]);
-    off_lo = og.lo; off_c = og.c; off_w = og.w;
-    ok = ok && og.ok;
-  }
-  ok = __all_sync(0xffffffffu, ok);
-  const int* table = a.table + (size_t)b * a.max_pages;
-  const size_t pool = (size_t)layer * a.n_pages * a.Hkv * a.pd.d;
-  const size_t chunk = pool * Y::kRow + (lane % Y::kChunks) * 16;      // this lane's, of row 0
-  const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.kc) + chunk;
-  const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.vc) + chunk;
-  const float* ks = E4M3 ? a.ks + pool : nullptr;
-  const float* vs = E4M3 ? a.vs + pool : nullptr;
-  bool lost = !inside;      // a position or page outside its range
-
-  // column 2c + e of this lane: token tok[e] of the block, query head sub[e] of the
-  // group, position qpos[e]
-  const int heads = min(a.per, a.G - grp * a.per), head0 = h * a.G + grp * a.per;
-  auto token_of = [&](int col) { return col * a.inv_per >> 8; };      // col / per, col < 8
-  int tok[2], sub[2], qpos[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    tok[e] = token_of(2 * c + e);
-    sub[e] = 2 * c + e - tok[e] * a.per;
-    if (sub[e] >= heads || tok[e] >= count) tok[e] = -1;
-    qpos[e] = tok[e] < 0 ? -(1 << 30) : pos0 + tok[e];
-  }
-
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float o[D / 16][4];
-#pragma unroll
-  for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_stages) +
-                        warp * (2 * Y::kBytes);
-  const int hrow = h * a.pd.d, page_rows = a.Hkv * a.pd.d;
-  // a team member's share: the last one has the offsets, the others every window_by-th
-  // pair of window tiles from the window_at-th on (0: none)
-  const bool offsets = !TEAM || warp == kWarps - 1;
-  const int window_by = !TEAM ? 1 : NT == 0 ? kWarps : offsets ? 0 : kWarps - 1;
-  const int window_at = TEAM && window_by ? warp : 0;
-  int n_far = a.n_off;                   // offsets that have rows of their own
-  unsigned near_lo = 0, near_hi = 0;     // distances 0..31 and 32..63 folded into the window
-
-  auto run = [&](auto kind) {
-    // 0: interpolated distances; integer ones: 1: 16 offsets a tile, 2: up to 8
-    // offsets left besides the folded ones, two tokens a tile
-    constexpr int KIND = decltype(kind)::value;
-    constexpr bool FLAT = KIND > 0;
-    constexpr int STEP = KIND == 2 ? 4 : KIND + 1;      // tokens of an offset stage
-    auto find = [&](int r, int& left) {
-      const int lp = quotient(a.pd, r), in = r - lp * a.pd.d;
-      int page = __ldg(table + lp);
-      if ((unsigned)page >= (unsigned)a.n_pages) {
-        lost = true;
-        page = 0;
-      }
-      left = a.pd.d - 1 - in;
-      return page * page_rows + hrow + in;
-    };
-    // Rows without a member take this row, the first token's own, with weight 0.
-    int unused;
-    const int fill = find(pos0, unused);
-
-    // ---- stages, in the order in which they are used: offset keys; window keys and
-    // values in turn; offset values ----
-    const int own = Y::own();
-    uint32_t in = ring, out = ring;
-    constexpr uint32_t kFlip = Y::kBytes;
-    auto stage_in = [&](const uint8_t* rows, int row, bool two, bool keys) {
-      Y::fill(in, own, rows, row, two);
-      if constexpr (E4M3) {
-        if (keys) copy4(in + Y::kScales + lane * 4, ks + row);
-        copy4(in + Y::kScales + 128 + lane * 4, vs + row);
-      }
-      in = ring + kFlip - (in - ring);
-    };
-    auto take = [&]() {      // the next stage to use, complete and visible to the warp
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      __syncwarp();
-      const uint32_t s = out;
-      out = ring + kFlip - (out - ring);
-      return s;
-    };
-    auto commit = []() { asm volatile("cp.async.commit_group;" ::: "memory"); };
-
-    // Offset stages. Interpolated: one per (token, tile pair); tile i of the pair
-    // has, for 8 offsets, rows a in 0..7 and rows b in 8..15. Integer distances: a
-    // tile holds 16 offsets of one token, or 8 of two.
-    int lo_[NT > 0 ? NT : 1], c_[NT > 0 ? NT : 1];      // of the row this lane looks up
-    const int ahead = KIND == 2 ? lane >> 3 : (KIND == 1 ? lane >> 4 : 0);      // for token t + ahead
-#pragma unroll
-    for (int pair = 0; pair < NT; ++pair) {
-      const int src = pair * 16 + (KIND == 2   ? lane & 7
-                                   : KIND == 1 ? lane & 15
-                                               : (lane >> 4) * 8 + (lane & 7));
-      const bool isb = !FLAT && (lane & 8);
-      lo_[pair] = __shfl_sync(0xffffffffu, off_lo, src) + isb;
-      c_[pair] = __shfl_sync(0xffffffffu, off_c, src);
-      if (!FLAT && __shfl_sync(0xffffffffu, off_w, src) == 0.f && isb)
-        c_[pair] = 0x7fffffff;      // no second row
-    }
-    Walk walk[NT > 0 ? NT : 1];
-    int next_t = 0;      // token of the next offset stage
-    auto offset_in = [&](int pair, bool keys) {
-      const int mine = next_t + ahead, p = pos0 + mine;
-      const bool there = c_[pair] <= p && mine < count;
-      Walk& w = walk[pair];
-      if (there) {
-        w.row += STEP;
-        w.left -= STEP;
-        if (w.left < 0) w.row = find(p - lo_[pair], w.left);
-      }
-      stage_in(keys ? kb : vb, there ? w.row : fill,
-               FLAT ? next_t + STEP / 2 < count : pair * 16 + 8 < a.n_off, keys);
-      if (pair == NT - 1) next_t += STEP;
-    };
-    auto restart = [&]() {      // the values go over the same tokens again
-      next_t = 0;
-#pragma unroll
-      for (int pair = 0; pair < NT; ++pair) walk[pair] = Walk();
-    };
-    const int n_off = (KIND == 2 && n_far == 0) || !offsets ? 0 : NT * ((count + STEP - 1) / STEP);
-
-    // Window tiles of 16 rows from `base`, the sinks as tile -1 before them.
-    const int last = pos0 + count - 1;
-    const int base = max(0, pos0 - (a.W - 1));
-    const int t_first = (a.S > 0 ? -1 : 0) + 2 * window_at, t_step = 2 * window_by;
-    const int t_past = !TEAM || window_by ? (last - base) / 16 + 1 : t_first;
-    int win_row = 0, win_t = t_first;      // rows and first tile of the last key stage
-    auto window_in = [&](int t0, bool keys) {
-      if (keys) {
-        const int t = t0 + (lane >> 4);      // this lane's tile
-        const int r = (t < 0 ? 0 : base + t * 16) + (lane & 15);
-        const bool there = r <= last && (t >= 0 || r < a.S);
-        win_row = find(there ? r : pos0, unused);
-        win_t = t0;
-      }
-      stage_in(keys ? kb : vb, win_row, win_t + 1 < t_past, keys);
-    };
-    // stage k of the whole order for k = 0 and 1, and from then on two ahead
-    // (a team's member may have no offsets, or no window)
-    const int n_win = t_first < t_past ? 2 : 0;      // its first key and value stage
-    auto after_keys = [&](int k) {      // stage k >= n_off, for k up to n_off + 1
-      if (k < n_off + n_win)
-        window_in(t_first, k == n_off);
-      else if (NT > 0 && k - n_win < 2 * n_off) {
-        if (k - n_win == n_off) restart();
-        offset_in(NT == 2 ? (k - n_win - n_off) & 1 : 0, false);
-      }
-    };
-    if (NT > 0 && n_off > 0)
-      offset_in(0, true);
-    else
-      after_keys(0);
-    commit();
-    if (NT > 0 && n_off > 1)
-      offset_in(NT - 1, true);
-    else
-      after_keys(1);
-    commit();
-
-    // Query fragments of column g. For e4m3 rows in fp16, times a power of two that
-    // brings the column's largest element to [2^14, 2^15): an element loses bits
-    // only where it is 2^28 times smaller.
-    uint32_t q[D / 8];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) q[i] = 0u;
-    {
-      const int t = token_of(g), hh = g - t * a.per;
-      if (hh < heads && t < count) {
-        const uint8_t* qp = reinterpret_cast<const uint8_t*>(
-            reinterpret_cast<const __nv_bfloat16*>(a.q) + layer * a.ql + (n0 + t) * a.qn +
-            (head0 + hh) * a.qh);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          if constexpr (E4M3) {      // elements 16 i + 4 c ..
-            load_words<8>(qp + i * 32 + c * 8, q + 2 * i);
-          } else {                   // 16 i + 2 c .. and 8 further
-            load_words<4>(qp + i * 32 + c * 4, q + 2 * i);
-            load_words<4>(qp + i * 32 + 16 + c * 4, q + 2 * i + 1);
-          }
-        }
-      }
-    }
-    float scale[2] = {a.scale * kLog2e, a.scale * kLog2e};      // of the lane's two columns
-    if constexpr (E4M3) {
-      __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&q[i])));
-      float top = fmaxf(__low2float(top2), __high2float(top2));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      int e = (int)(__float_as_uint(top) >> 23) - 127;          // 2^e <= top < 2^(e+1)
-      e = e < -100 || e > 127 ? 14 : e;                         // zeros, infinities: as they are
-      const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-      const float down = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) q[i] = pack16<true>(bf16lo(q[i]) * up, bf16hi(q[i]) * up);
-      scale[0] *= __shfl_sync(0xffffffffu, down, 8 * c);
-      scale[1] *= __shfl_sync(0xffffffffu, down, 8 * c + 4);
-    }
-    const uint32_t at_k = Y::lane_at(false), at_v = Y::lane_at(true);
-    // scales of the stage's rows i * 16 + half * 8 + g: keys 0, values 1
-    auto row_scale = [&](uint32_t stage, int which, int i, int half) {
-      return load_shared(stage + Y::kScales + which * 128 + (i * 16 + half * 8 + g) * 4);
-    };
-    auto log_scale = [](float x) {      // 2^-100 at least; NaN does not matter here
-      float y;
-      asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(fabsf(x), 7.9e-31f)));
-      return y;
-    };
-
-    // Running reference m and sum l of each of the lane's columns; o the outputs
-    // times l. For e4m3 rows the reference is the maximum of score + log2(value
-    // scale): the weights that go into P V, probability * value scale, are then at
-    // most 1 and fit fp16 whatever the scales.
-    constexpr int NS = NT > 0 && KIND != 2 ? 2 * NT : 1;
-    float beta[2] = {0.f, 0.f};
-    if (NT > 0 && a.beta) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (tok[e] >= 0)
-          beta[e] = kLog2e * __ldg(a.beta + ((size_t)layer * a.N + n0 + tok[e]) * a.Hq + head0 +
-                                   sub[e]);
-    }
-    // a folded offset is its window row a second time: log2(1 + 2^beta) more score
-    [[maybe_unused]] float extra[2] = {0.f, 0.f};
-    if (KIND == 2 && (near_lo | near_hi)) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)      // (from the larger of the two terms)
-        extra[e] = fmaxf(beta[e], 0.f) + log2f(1.f + exp2f(-fabsf(beta[e])));
-    }
-    [[maybe_unused]] float sig[NS][2], wg[NS];      // scores, and weights of row b, of offset 8 i + g
-    if constexpr (NT > 0) {
-      // ---- offset scores: a lane keeps its own columns' ----
-      float vl[NS][2];
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        wg[i] = FLAT ? 0.f : __shfl_sync(0xffffffffu, off_w, i * 8 + g);
-        sig[i][0] = sig[i][1] = vl[i][0] = vl[i][1] = 0.f;
-      }
-      int k = 2;      // the stage after the next
-      for (int t = 0; k < n_off + 2; t += STEP) {
-#pragma unroll
-        for (int pair = 0; pair < NT; ++pair, ++k) {
-          const bool second = FLAT ? t + STEP / 2 < count : pair * 16 + 8 < a.n_off;
-          const uint32_t stage = take();
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (i == 1 && !second) continue;
-            float s[4], va = 0.f, vc = 0.f, ka = 1.f, kc = 1.f;
-            Y::scores(stage, i, at_k, q, s);
-            if constexpr (E4M3) {
-              ka = row_scale(stage, 0, i, 0);
-              kc = row_scale(stage, 0, i, 1);
-              va = log_scale(row_scale(stage, 1, i, 0));
-              vc = log_scale(row_scale(stage, 1, i, 1));
-            }
-            if constexpr (KIND == 2) {      // rows g and g + 8: offset g of two tokens
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                if (tok[e] == t + 2 * i) {
-                  sig[0][e] = s[e] * ka;
-                  vl[0][e] = va;
-                }
-                if (tok[e] == t + 2 * i + 1) {
-                  sig[0][e] = s[2 + e] * kc;
-                  vl[0][e] = vc;
-                }
-              }
-            } else if constexpr (FLAT) {      // offsets 16 pair + g and 8 further
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (tok[e] == t + i) {
-                  sig[2 * pair][e] = s[e] * ka;
-                  sig[2 * pair + 1][e] = s[2 + e] * kc;
-                  vl[2 * pair][e] = va;
-                  vl[2 * pair + 1][e] = vc;
-                }
-            } else {      // (a weight of 0 times a non-finite score: found at the end)
-              const float wb = wg[2 * pair + i] * kc, wa = (1.f - wg[2 * pair + i]) * ka;
-              if (wg[2 * pair + i] != 0.f) va = fmaxf(va, vc);
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (tok[e] == t) {
-                  sig[2 * pair + i][e] = fmaf(wb, s[2 + e], wa * s[e]);
-                  vl[2 * pair + i][e] = va;
-                }
-            }
-          }
-          __syncwarp();
-          if (k < n_off)
-            offset_in(pair, true);
-          else
-            after_keys(k);
-          commit();
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const int c_of = __shfl_sync(0xffffffffu, off_c, i * 8 + g);
-        const int cc = offsets ? c_of : 0x7fffffff;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          sig[i][e] = cc <= qpos[e] ? fmaf(sig[i][e], scale[e], beta[e]) : -INFINITY;
-          m[e] = fmaxf(m[e], E4M3 ? sig[i][e] + vl[i][e] : sig[i][e]);
-        }
-      }
-#pragma unroll
-      for (int d = 4; d <= 16; d <<= 1) {
-        m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], d));
-        m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], d));
-      }
-    }
-
-    // ---- window and sinks, two tiles of 16 rows at a time ----
-    for (int t0 = t_first; t0 < t_past; t0 += t_step) {
-      const bool second = t0 + 1 < t_past, more = t0 + t_step < t_past;
-      float s[2][4], nm[2] = {-INFINITY, -INFINITY};
-      uint32_t stage = take();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (i == 1 && !second) {
-          s[1][0] = s[1][1] = s[1][2] = s[1][3] = -INFINITY;
-          continue;
-        }
-        Y::scores(stage, i, at_k, q, s[i]);
-        const int t = t0 + i;
-        float ka[2] = {scale[0], scale[1]}, kc[2] = {scale[0], scale[1]}, va = 0.f, vc = 0.f;
-        if constexpr (E4M3) {
-          const float x0 = row_scale(stage, 0, i, 0), x1 = row_scale(stage, 0, i, 1);
-          ka[0] *= x0; ka[1] *= x0; kc[0] *= x1; kc[1] *= x1;
-          va = log_scale(row_scale(stage, 1, i, 0));
-          vc = log_scale(row_scale(stage, 1, i, 1));
-        }
-        // lags of rows g and g + 8 from the two columns' positions (negative, so
-        // large unsigned, where there is no column); sinks have no far edge, and
-        // beyond the last one stand at a position past all
-        const int r0 = t < 0 ? (g < a.S ? g : 1 << 29) : base + t * 16 + g;
-        const int r1 = t < 0 ? (g + 8 < a.S ? g + 8 : 1 << 29) : r0 + 8;
-        const unsigned far = t < 0 ? 0x7fffffffu : (unsigned)a.W;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          s[i][e] = (unsigned)(qpos[e] - r0) < far ? s[i][e] * ka[e] : -INFINITY;
-          s[i][2 + e] = (unsigned)(qpos[e] - r1) < far ? s[i][2 + e] * kc[e] : -INFINITY;
-          if (KIND == 2 && (near_lo | near_hi)) {      // (uniform)
-            const int l0 = qpos[e] - r0, l1 = qpos[e] - r1;
-            if (t >= 0 && (unsigned)l0 < 64u && ((l0 < 32 ? near_lo : near_hi) >> (l0 & 31) & 1u))
-              s[i][e] += extra[e];
-            if (t >= 0 && (unsigned)l1 < 64u && ((l1 < 32 ? near_lo : near_hi) >> (l1 & 31) & 1u))
-              s[i][2 + e] += extra[e];
-          }
-          nm[e] = fmaxf(nm[e], E4M3 ? fmaxf(s[i][e] + va, s[i][2 + e] + vc)
-                                    : fmaxf(s[i][e], s[i][2 + e]));
-        }
-      }
-      __syncwarp();
-      if (more)
-        window_in(t0 + t_step, true);
-      else if (NT > 0 && n_off > 0) {
-        restart();
-        offset_in(0, false);
-      }
-      commit();
-#pragma unroll
-      for (int d = 4; d <= 16; d <<= 1) {
-        nm[0] = fmaxf(nm[0], __shfl_xor_sync(0xffffffffu, nm[0], d));
-        nm[1] = fmaxf(nm[1], __shfl_xor_sync(0xffffffffu, nm[1], d));
-      }
-      if (__any_sync(0xffffffffu, nm[0] > m[0] || nm[1] > m[1])) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          nm[e] = fmaxf(nm[e], m[e]);
-          const float f = exp2_approx(m[e] - (nm[e] == -INFINITY ? 0.f : nm[e]));
-          m[e] = nm[e];
-          l[e] *= f;
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            o[j][e] *= f;
-            o[j][2 + e] *= f;
-          }
-        }
-      }
-      const float z0 = m[0] == -INFINITY ? 0.f : m[0], z1 = m[1] == -INFINITY ? 0.f : m[1];
-      stage = take();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (i == 1 && !second) continue;
-        float p[4] = {exp2_approx(s[i][0] - z0), exp2_approx(s[i][1] - z1),
-                      exp2_approx(s[i][2] - z0), exp2_approx(s[i][3] - z1)};
-        l[0] += p[0] + p[2];
-        l[1] += p[1] + p[3];
-        if constexpr (E4M3) {
-          const float va = row_scale(stage, 1, i, 0), vc = row_scale(stage, 1, i, 1);
-          p[0] *= va; p[1] *= va; p[2] *= vc; p[3] *= vc;
-        }
-        Y::add(stage, i, at_v, transpose8(pack16<E4M3>(p[0], p[1])),
-               transpose8(pack16<E4M3>(p[2], p[3])), o);
-      }
-      __syncwarp();
-      if (more)
-        window_in(t0 + t_step, false);
-      else if (NT > 0 && n_off > 1)
-        offset_in(NT - 1, false);
-      commit();
-    }
-
-    // ---- offset values ----
-    if constexpr (NT > 0) {
-      const float z0 = m[0] == -INFINITY ? 0.f : m[0], z1 = m[1] == -INFINITY ? 0.f : m[1];
-      // P^T of all columns (plain rows): lane (g, c) has column g, rows 2c and 2c + 1;
-      // a token's product takes its own columns of it
-      [[maybe_unused]] uint32_t pa[NS], pb[NS];
-      const int tok_g = token_of(g);
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        sig[i][0] = exp2_approx(sig[i][0] - z0);
-        sig[i][1] = exp2_approx(sig[i][1] - z1);
-        l[0] += sig[i][0];
-        l[1] += sig[i][1];
-        if constexpr (!E4M3) {
-          const float wb = wg[i], wa = 1.f - wb;
-          pa[i] = transpose8(pack_bf16x2(sig[i][0] * wa, sig[i][1] * wa));
-          if (!FLAT) pb[i] = transpose8(pack_bf16x2(sig[i][0] * wb, sig[i][1] * wb));
-        }
-      }
-      int k = 2;
-      for (int t = 0; k < n_off + 2; t += STEP) {
-#pragma unroll
-        for (int pair = 0; pair < NT; ++pair, ++k) {
-          const bool second = FLAT ? t + STEP / 2 < count : pair * 16 + 8 < a.n_off;
-          const uint32_t stage = take();
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (i == 1 && !second) continue;
-            // tokens and offsets of rows 0..7 and 8..15
-            const int at = KIND == 2 ? t + 2 * i : (FLAT ? t + i : t);
-            const int bt = KIND == 2 ? at + 1 : at;
-            const int ia = KIND == 2 ? 0 : (FLAT ? 2 * pair : 2 * pair + i);
-            const int ib = KIND == 1 ? 2 * pair + 1 : ia;
-            uint32_t p0, p1;
-            if constexpr (E4M3) {
-              const float wb = FLAT ? 1.f : wg[ia], wa = FLAT ? 1.f : 1.f - wb;
-              const float va = row_scale(stage, 1, i, 0) * wa, vc = row_scale(stage, 1, i, 1) * wb;
-              p0 = transpose8(pack16<true>(tok[0] == at ? sig[ia][0] * va : 0.f,
-                                           tok[1] == at ? sig[ia][1] * va : 0.f));
-              p1 = transpose8(pack16<true>(tok[0] == bt ? sig[ib][0] * vc : 0.f,
-                                           tok[1] == bt ? sig[ib][1] * vc : 0.f));
-            } else {
-              p0 = tok_g == at ? pa[ia] : 0u;
-              p1 = tok_g == bt ? (FLAT ? pa[ib] : pb[ib]) : 0u;
-            }
-            Y::add(stage, i, at_v, p0, p1, o);
-          }
-          __syncwarp();
-          if (k < n_off) offset_in(pair, false);
-          commit();
-        }
-      }
-    }
-  };
-  if (ok) {
-    if (NT == 0) {
-      run(std::integral_constant<int, 1>());
-    } else if (!__all_sync(0xffffffffu, off_w == 0.f)) {
-      run(std::integral_constant<int, 0>());
-    } else {
-      // Integer distances: an offset inside the window is a window row a second time.
-      // Such offsets (the first of each distance) are folded into the window's scores
-      // where that leaves at most 8 others, which then go two tokens to a tile.
-      if constexpr (NT == 1) {
-        const bool listed = lane < a.n_off;
-        const unsigned same = __match_any_sync(0xffffffffu, listed ? off_lo : -1 - lane);
-        const bool near = listed && off_lo < min(a.W, 64) && __ffs(same) == lane + 1;
-        unsigned far = __ballot_sync(0xffffffffu, listed && !near);
-        if (!TEAM && count > 2 && (far == 0 || (a.n_off > 8 && __popc(far) <= 8))) {
-          near_lo = __reduce_or_sync(0xffffffffu, near && off_lo < 32 ? 1u << off_lo : 0u);
-          near_hi = __reduce_or_sync(0xffffffffu, near && off_lo >= 32 ? 1u << (off_lo & 31) : 0u);
-        } else {
-          far = __ballot_sync(0xffffffffu, listed);
-        }
-        n_far = __popc(far);
-        if (n_far <= 8) {      // the others, in order, to lanes 0 .. n_far - 1
-          int* list = reinterpret_cast<int*>(s_stages + warp * (2 * Y::kBytes));
-          if (far >> lane & 1u) list[__popc(far & ((1u << lane) - 1u))] = off_lo;
-          __syncwarp();
-          off_lo = lane < n_far ? list[lane] : 0;
-          off_c = lane < n_far ? off_lo : 0x7fffffff;
-          __syncwarp();
-        }
-      }
-      if constexpr (NT == 1) {
-        if (n_far <= 8)
-          run(std::integral_constant<int, 2>());
-        else
-          run(std::integral_constant<int, 1>());
-      } else {
-        run(std::integral_constant<int, 1>());
-      }
-    }
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  if constexpr (TEAM) {      // the first member joins the parts
-    constexpr int kPart = D / 4 + 4;      // floats of a lane's part
-    static_assert(kPart * 32 * 4 <= 2 * Y::kBytes, "a part fits a warp's stages");
-    float* mine = reinterpret_cast<float*>(s_stages + warp * (2 * Y::kBytes)) + lane;
-    __syncwarp();
-    if (warp > 0) {
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mine[(4 * j + e) * 32] = o[j][e];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mine[(D / 4 + e) * 32] = m[e];
-        mine[(D / 4 + 2 + e) * 32] = l[e];
-      }
-      if (__any_sync(0xffffffffu, lost) && lane == 0) {
-        mine[(D / 4) * 32] = __int_as_float(0x7fc00000);      // tells the first member
-        atomicOr(&g_chunk_err, kErrPage);
-      }
-    }
-    __syncthreads();      // (the returns before are the same for the whole CTA)
-    if (warp > 0) return;
-    for (int w = 1; w < kWarps; ++w) {
-      const float* part = reinterpret_cast<const float*>(s_stages + w * (2 * Y::kBytes)) +
-                          lane;
-      lost = lost || __shfl_sync(0xffffffffu, part[(D / 4) * 32] != part[(D / 4) * 32], 0);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float mp = part[(D / 4 + e) * 32], top = fmaxf(m[e], mp);
-        const float z = top == -INFINITY ? 0.f : top;
-        const float f = exp2_approx(m[e] - z), fp = exp2_approx(mp - z);
-        m[e] = top;
-        l[e] = l[e] * f + part[(D / 4 + 2 + e) * 32] * fp;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          o[j][e] = o[j][e] * f + part[(4 * j + e) * 32] * fp;
-          o[j][2 + e] = o[j][2 + e] * f + part[(4 * j + 2 + e) * 32] * fp;
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int d = 4; d <= 16; d <<= 1) {
-    l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
-    l[1] += __shfl_xor_sync(0xffffffffu, l[1], d);
-  }
-  const bool nan = __any_sync(0xffffffffu, lost) || !ok;
-
-  // A weight of 0 does not hide an infinity or a NaN: when an output is not
-  // finite, the block's queries are computed again from their own members alone.
-  float odd[2] = {l[0], l[1]};      // times 0: 0 for finite values only
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    odd[e] *= 0.f;
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j)
-      odd[e] = fmaf(o[j][e], 0.f, fmaf(o[j][2 + e], 0.f, odd[e]));
-  }
-  if (!nan && __any_sync(0xffffffffu, (tok[0] >= 0 && odd[0] != 0.f) ||
-                                          (tok[1] >= 0 && odd[1] != 0.f))) {
-    for (int col = 0; col < count * a.per; ++col) {
-      const int t = token_of(col), hh = col - t * a.per;
-      if (hh < heads)
-        one_query<__nv_bfloat16, D, E4M3>(a, layer, head0 + hh, n0 + t, b, pos0 + t, true);
-    }
-    return;
-  }
-
-  // Outputs through shared memory: one row per column, 16 bytes apart in banks,
-  // then 16 bytes a lane of consecutive head dims.
-  constexpr int kOut = D * 2 + 16;
-  uint8_t* out = s_stages + warp * (2 * Y::kBytes);
-  static_assert(8 * kOut <= 2 * Y::kBytes, "the output tile fits the stages");
-  __syncwarp();
-  const float bad = __int_as_float(0x7fc00000);
-  const float inv0 = nan ? bad : 1.f / l[0], inv1 = nan ? bad : 1.f / l[1];
-#pragma unroll
-  for (int j = 0; j < D / 16; ++j) {
-    if constexpr (E4M3) {      // head dims 16 j + 2 g and the next
-      *reinterpret_cast<uint32_t*>(out + (2 * c) * kOut + (16 * j + 2 * g) * 2) =
-          pack_bf16x2(o[j][0] * inv0, o[j][2] * inv0);
-      *reinterpret_cast<uint32_t*>(out + (2 * c + 1) * kOut + (16 * j + 2 * g) * 2) =
-          pack_bf16x2(o[j][1] * inv1, o[j][3] * inv1);
-    } else {                   // transposed: column g, head dims 2c and 2c + 1 of eight
-      *reinterpret_cast<uint32_t*>(out + g * kOut + (16 * j + 2 * c) * 2) =
-          transpose8(pack_bf16x2(o[j][0] * inv0, o[j][1] * inv1));
-      *reinterpret_cast<uint32_t*>(out + g * kOut + (16 * j + 8 + 2 * c) * 2) =
-          transpose8(pack_bf16x2(o[j][2] * inv0, o[j][3] * inv1));
-    }
-  }
-  __syncwarp();
-  constexpr int kPer = D / 8;      // 16-byte chunks of a row
-  const size_t out0 = ((size_t)layer * a.N + n0) * a.Hq + head0;
-#pragma unroll
-  for (int i = 0; i < 8 * kPer / 32 || i == 0; ++i) {
-    const int id = i * 32 + lane, col = id / kPer, t = token_of(col), hh = col - t * a.per;
-    if (id < 8 * kPer && t < count && hh < heads)
-      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.o) +
-                                (out0 + t * a.Hq + hh) * D + (id % kPer) * 8) =
-          *reinterpret_cast<const uint4*>(out + col * kOut + (id % kPer) * 16);
-  }
-  if (a.lse && g == 0) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (tok[e] >= 0)
-        a.lse[out0 + tok[e] * a.Hq + sub[e]] = nan ? bad : kLn2 * (m[e] + log2f(l[e]));
-  }
-  if (__any_sync(0xffffffffu, lost) && lane == 0) atomicOr(&g_chunk_err, kErrPage);
-}
-
-// ---------------------------------------------------------------------------
-// 32-bit queries, and the queries that meet infinities or NaN.
-
-// NE consecutive elements of a cache row from element e0, as stored.
-template <bool E4M3, bool BF16, int NE>
-__device__ __forceinline__ void load_part(const uint8_t* base, int D, int row, int e0,
-                                          float (&x)[NE]) {
-  if constexpr (E4M3) {
-    const uint8_t* p = base + (size_t)row * D + e0;
-    if constexpr (NE == 1) {
-      float unused;
-      e4m3x2_to_float2(__ldg(p), x[0], unused);
-    } else {
-      constexpr int STEP = NE < 16 ? NE : 16, NW = STEP < 4 ? 1 : STEP / 4;
-#pragma unroll
-      for (int i = 0; i < NE / STEP; ++i) {
-        uint32_t u[NW];
-        load_words<STEP>(p + i * STEP, u);
-#pragma unroll
-        for (int j = 0; j < STEP / 2; ++j)
-          e4m3x2_to_float2((u[j / 2] >> (16 * (j & 1))) & 0xffffu, x[i * STEP + 2 * j],
-                           x[i * STEP + 2 * j + 1]);
-      }
-    }
-  } else if constexpr (BF16) {
-    load_row<__nv_bfloat16, NE>(reinterpret_cast<const __nv_bfloat16*>(base) + (size_t)row * D + e0,
-                                x);
-  } else {
-    const float* p = reinterpret_cast<const float*>(base) + (size_t)row * D + e0;
-    if constexpr (NE == 1)
-      x[0] = __ldg(p);
-    else if constexpr (NE == 2) {
-      const float2 u = __ldg(reinterpret_cast<const float2*>(p));
-      x[0] = u.x; x[1] = u.y;
-    } else
-      load_row<float, NE>(p, x);
-  }
-}
-
-// One query (token row n of sequence b at position pos, query head hq) by one
-// warp: members 32 at a time, and no row but its members' is touched.
-template <typename QT, int D, bool E4M3>
-__device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, int n, int b,
-                                       int pos, bool inside) {
-  constexpr bool BF16 = !E4M3 && sizeof(QT) == 2;
-  constexpr int QE = D / 4;                        // elements of a row per quad lane
-  constexpr int VE = D >= 32 ? D / 32 : 1;         // value elements per lane
-  constexpr int SPLIT = D >= 32 ? 1 : 2;           // D = 16: two members at a time
-  const int lane = threadIdx.x & 31, part = lane & 3, mm = lane >> 2;
-  const int h = hq / a.G;
-
-  int off_lo = 0, off_c = 0x7fffffff;
-  float off_w = 0.f;
-  bool ok = inside;
-  if (lane < a.n_off) {
-    const OffGeo og = offset_geometry(__ldg(a.alpha + layer), a.f[lane]);
-    off_lo = og.lo; off_c = og.c; off_w = og.w;
-    ok = ok && og.ok;
-  }
-  ok = __all_sync(0xffffffffu, ok);
-  bool lost = !inside;
-  const int* table = a.table + (size_t)b * a.max_pages;
-  const size_t pool = (size_t)layer * a.n_pages * a.Hkv * a.pd.d;
-  constexpr int kElt = E4M3 ? 1 : (int)sizeof(QT);
-  const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.kc) + pool * D * kElt;
-  const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.vc) + pool * D * kElt;
-
-  float q[QE];
-  load_row<QT, QE>(reinterpret_cast<const QT*>(a.q) + layer * a.ql + n * a.qn + hq * a.qh +
-                       part * QE, q);
-  const size_t at = ((size_t)layer * a.N + n) * a.Hq + hq;
-  const float beta = a.beta ? __ldg(a.beta + at) : 0.f;
-  const int nw = min(a.W, pos + 1), ns = min(a.S, pos + 1);
-  const int total = ok ? nw + ns + a.n_off : 0;
-
-  float m = -INFINITY, l = 0.f, o[VE];
-#pragma unroll
-  for (int i = 0; i < VE; ++i) o[i] = 0.f;
-  const int d0 = (D >= 32 ? lane : (lane & 15)) * VE;
-
-  for (int m0 = 0; m0 < total; m0 += 32) {
-    // lane's member m0 + lane: rows, weights
-    const int mem = m0 + lane;
-    const int k = mem - nw - ns;
-    const int lo = __shfl_sync(0xffffffffu, off_lo, k & 31);
-    const int cc = __shfl_sync(0xffffffffu, off_c, k & 31);
-    const float w = __shfl_sync(0xffffffffu, off_w, k & 31);
-    int ra = -1, rb = -1;
-    if (mem < nw) {
-      ra = pos - mem;
-    } else if (k < 0) {
-      ra = mem - nw;
-    } else if (k < a.n_off && cc <= pos) {
-      ra = pos - lo;
-      if (w != 0.f) rb = ra - 1;
-    }
-    float wa = 1.f, wb = 0.f;
-    const bool off = k >= 0;
-    if (rb >= 0) { wa = 1.f - w; wb = w; }
-    if (ra >= 0) { ra = pool_row(table, a.pd, ra, a.n_pages, a.Hkv, h); lost |= ra < 0; }
-    if (rb >= 0) { rb = pool_row(table, a.pd, rb, a.n_pages, a.Hkv, h); lost |= rb < 0; }
-    float ka = wa, kc = wb, va = wa, vc = wb;
-    if constexpr (E4M3) {
-      if (ra >= 0) { ka *= __ldg(a.ks + pool + ra); va *= __ldg(a.vs + pool + ra); }
-      if (rb >= 0) { kc *= __ldg(a.ks + pool + rb); vc *= __ldg(a.vs + pool + rb); }
-    }
-    // scores: 8 members at a time, four lanes each
-    float s = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int ia = __shfl_sync(0xffffffffu, ra, i * 8 + mm);
-      const int ib = __shfl_sync(0xffffffffu, rb, i * 8 + mm);
-      const float xa = __shfl_sync(0xffffffffu, ka, i * 8 + mm);
-      const float xb = __shfl_sync(0xffffffffu, kc, i * 8 + mm);
-      float dot = 0.f;
-      if (ia >= 0) {
-        float x[QE];
-        load_part<E4M3, BF16, QE>(kb, D, ia, part * QE, x);
-        float t = 0.f;
-#pragma unroll
-        for (int e = 0; e < QE; ++e) t = fmaf(q[e], x[e], t);
-        dot = t * xa;
-      }
-      if (ib >= 0) {
-        float x[QE];
-        load_part<E4M3, BF16, QE>(kb, D, ib, part * QE, x);
-        float t = 0.f;
-#pragma unroll
-        for (int e = 0; e < QE; ++e) t = fmaf(q[e], x[e], t);
-        dot = fmaf(t, xb, dot);
-      }
-      dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-      dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-      const float mine = __shfl_sync(0xffffffffu, dot, (lane & 7) * 4);
-      if ((lane >> 3) == i) s = mine;
-    }
-    s = ra >= 0 ? (s * a.scale + (off ? beta : 0.f)) * kLog2e : -INFINITY;
-    float nm = s;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
-    nm = fmaxf(m, nm);
-    const float z = nm == -INFINITY ? 0.f : nm;
-    const float f = exp2f(m - z), p = exp2f(s - z);
-    m = nm;
-    l = l * f + p;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) o[i] *= f;
-    va *= p;
-    vc *= p;
-    const int here = min(32, total - m0);
-    for (int i = 0; i < here; i += SPLIT) {
-      const int src = i + (SPLIT == 2 ? lane >> 4 : 0);
-      const int ia = __shfl_sync(0xffffffffu, ra, src & 31);
-      const int ib = __shfl_sync(0xffffffffu, rb, src & 31);
-      const float xa = __shfl_sync(0xffffffffu, va, src & 31);
-      const float xb = __shfl_sync(0xffffffffu, vc, src & 31);
-      if (ia >= 0) {
-        float x[VE];
-        load_part<E4M3, BF16, VE>(vb, D, ia, d0, x);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) o[e] = fmaf(xa, x[e], o[e]);
-      }
-      if (ib >= 0) {
-        float x[VE];
-        load_part<E4M3, BF16, VE>(vb, D, ib, d0, x);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) o[e] = fmaf(xb, x[e], o[e]);
-      }
-    }
-  }
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  if constexpr (SPLIT == 2) o[0] += __shfl_xor_sync(0xffffffffu, o[0], 16);
-  const bool nan = __any_sync(0xffffffffu, lost) || !ok;
-  const float bad = __int_as_float(0x7fc00000);
-  const float inv = nan ? bad : 1.f / l;
-  if (D >= 32 || lane < 16) {
-#pragma unroll
-    for (int e = 0; e < VE; ++e) o[e] *= inv;
-    store_row<QT, VE>(reinterpret_cast<QT*>(a.o) + at * D + d0, o);
-  }
-  if (lane == 0 && a.lse) a.lse[at] = nan ? bad : kLn2 * m + logf(l);
-  if (lost) atomicOr(&g_chunk_err, kErrPage);
-}
-
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const __grid_constant__ ChunkArgs a) {
-  const int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (n >= a.N) return;
-  const int b = find_sequence(a.cu, a.B, 0, n);
-  const int first = __ldg(a.cu + b);
-  if (first < 0 || n < first || n >= __ldg(a.cu + b + 1)) return;
-  const long long posl = (long long)__ldg(a.cached + b) + (n - first);
-  const bool inside = posl >= 0 && posl < (long long)a.max_pages * a.pd.d;
-  one_query<float, D, E4M3>(a, blockIdx.z, blockIdx.y, n, b, inside ? (int)posl : 0, inside);
-}
-
-template <int D, bool E4M3, int NT, bool TEAM>
-cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t st) {
-  const dim3 grid(TEAM ? a.blocks : (a.blocks + kWarps - 1) / kWarps, a.Hkv * a.groups, a.L);
-  constexpr int smem = kWarps * 2 * Stage<D, E4M3>::kBytes;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        k_chunk_tc<D, E4M3, NT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  k_chunk_tc<D, E4M3, NT, TEAM><<<grid, kWarps * 32, smem, st>>>(a);
-  return cudaSuccess;
-}
-
-template <int D, bool E4M3, int NT>
-cudaError_t launch_nt(const ChunkArgs& a, cudaStream_t st) {
-  return a.team ? launch_tc<D, E4M3, NT, true>(a, st) : launch_tc<D, E4M3, NT, false>(a, st);
-}
-
-template <int D, bool E4M3>
-cudaError_t launch_t(const ChunkArgs& a, bool f32, cudaStream_t st) {
-  cudaError_t e = cudaSuccess;
-  trace_mark("chunk_attn", st, true);
-  if (f32) {
-    const dim3 grid((a.N + kWarps - 1) / kWarps, a.Hq, a.L);
-    k_chunk_f32<D, E4M3><<<grid, kWarps * 32, 0, st>>>(a);
-  } else {
-    e = a.n_off == 0    ? launch_nt<D, E4M3, 0>(a, st)
-        : a.n_off <= 16 ? launch_nt<D, E4M3, 1>(a, st)
-                        : launch_nt<D, E4M3, 2>(a, st);
-  }
-  trace_mark("chunk_attn", st, false);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-}  // namespace
 
 cudaError_t launch_chunk_attn(const PagedProblem& p, const PagedPtrs& c, const ChunkPtrs& x,
                               cudaStream_t st) {
@@ -1178,18 +34,21 @@ cudaError_t launch_chunk_attn(const PagedProblem& p, const PagedPtrs& c, const C
   a.team = (rows + 15) / 16 + (x.S > 0) >= 3 && warps <= 148 * 4;
   const bool f32 = p.dtype == SA_DTYPE_F32, q8 = p.format == SA_CACHE_E4M3;
   switch (p.D) {
-    case 16: return q8 ? launch_t<16, true>(a, f32, st) : launch_t<16, false>(a, f32, st);
-    case 32: return q8 ? launch_t<32, true>(a, f32, st) : launch_t<32, false>(a, f32, st);
-    case 64: return q8 ? launch_t<64, true>(a, f32, st) : launch_t<64, false>(a, f32, st);
-    default: return q8 ? launch_t<128, true>(a, f32, st) : launch_t<128, false>(a, f32, st);
+    case 16: return launch_chunk_of<16>(a, f32, q8, st);
+    case 32: return launch_chunk_of<32>(a, f32, q8, st);
+    case 64: return launch_chunk_of<64>(a, f32, q8, st);
+    default: return launch_chunk_of<128>(a, f32, q8, st);
   }
 }
 
 cudaError_t chunk_read_error(unsigned* out, bool clear) {
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_chunk_err, sizeof(unsigned));
-  if (e != cudaSuccess || !clear || *out == 0) return e;
-  const unsigned zero = 0;
-  return cudaMemcpyToSymbol(g_chunk_err, &zero, sizeof(unsigned));
+  unsigned w[4] = {0, 0, 0, 0};
+  cudaError_t e = chunk_error_of<16>(w, clear);
+  if (e == cudaSuccess) e = chunk_error_of<32>(w + 1, clear);
+  if (e == cudaSuccess) e = chunk_error_of<64>(w + 2, clear);
+  if (e == cudaSuccess) e = chunk_error_of<128>(w + 3, clear);
+  *out = w[0] | w[1] | w[2] | w[3];
+  return e;
 }
 
 }  // namespace sa

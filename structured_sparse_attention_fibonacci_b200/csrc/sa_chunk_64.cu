@@ -1,0 +1,8 @@
+// The chunk attention's kernels for head dim 64.
+#define SA_CHUNK_KERNELS
+#include "sa_chunk.cuh"
+
+namespace sa {
+template cudaError_t launch_chunk_of<64>(const ChunkArgs&, bool, bool, cudaStream_t);
+template cudaError_t chunk_error_of<64>(unsigned*, bool);
+}  // namespace sa

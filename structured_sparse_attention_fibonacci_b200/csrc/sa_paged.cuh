@@ -81,13 +81,7 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
   return __int_as_float((e + 127) << 23);
 }
 
-// Two e4m3 codes (low byte first) to two bf16 values; exact, NaN kept.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
-  uint32_t h;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"(two));
-  const __half2 x = *reinterpret_cast<const __half2*>(&h);
-  return pack_bf16x2(__low2float(x), __high2float(x));
-}
+// Two e4m3 codes (low byte first) to fp32; exact, NaN kept.
 __device__ __forceinline__ void e4m3x2_to_float2(uint32_t two, float& a, float& b) {
   uint32_t h;
   asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"(two));

@@ -99,6 +99,14 @@ for n, (offs, alphas, W) in enumerate([
                       [0, 130, 9], [21, 1, 14], 0, 0))
 
 
+# Interpolated distances, one query head per key head: tokens share each other's rows
+for D in (16, 32, 64, 128):
+    for fmt in ("plain", "e4m3"):
+        for n, (offs, W) in enumerate(((FIB, 12), (MANY, 5), ((1,), 20), ((3, 900, 1, 2, 6), 1))):
+            CHUNK.append((f"shared_{n}_{fmt}_{D}", BF, fmt, D, 2, 2, (16, 5, 64, 1)[n], W, 2 * (n % 2), offs,
+                          [0.77, 1.37], [0, 300, 77, 12], [37, 9, 4, 3], n, n))
+
+
 @pytest.mark.parametrize("prior", [False, True], ids=["", "prior"])
 @pytest.mark.parametrize("case", CHUNK, ids=[c[0] for c in CHUNK])
 def test_chunk_matches_the_plain_form(case, prior):
