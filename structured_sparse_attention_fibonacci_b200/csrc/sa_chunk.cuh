@@ -272,30 +272,36 @@ struct Stage {
     const int half = v ? mi >> 1 : mi & 1, chunk = v ? mi & 1 : mi >> 1;
     return place((lane & 7) + 8 * half, kChunks > 1 ? chunk : 0);
   }
-  // S^T of a tile's 16 keys with the block's 8 columns.
-  template <int OFFSET>
+  // S^T of N tiles' 16 keys each, STEP bytes from one to the next, with the block's 8
+  // columns: the tiles in turn, so that a product does not wait for the one before.
+  template <int N, int STEP>
   static __device__ __forceinline__ void scores(uint32_t stage, uint32_t at,
-                                                const uint32_t (&q)[D / 8], float (&s)[4]) {
-    s[0] = s[1] = s[2] = s[3] = 0.f;
-    if constexpr (!E4M3) {
+                                                const uint32_t (&q)[D / 8], float (&s)[N][4]) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {      // 16 elements: two chunks
-        uint32_t r[4];
-        ldmatrix4<false, OFFSET>(stage + (at ^ (i << 5)), r);
-        mma16816<false>(s, r[0], r[1], r[2], r[3], q[2 * i], q[2 * i + 1]);
-      }
-    } else {
+    for (int t = 0; t < N; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+    constexpr int kPairs = (kChunks + 1) / 2;      // chunk pairs: 16 elements, 32 codes
 #pragma unroll
-      for (int i = 0; i < (kChunks + 1) / 2; ++i) {      // 16 codes a chunk, two chunks
-        uint32_t r[4];
-        ldmatrix4<false, OFFSET>(stage + (at ^ (i << 5)), r);
+    for (int i = 0; i < kPairs; ++i) {
+      uint32_t r[N][4];
+      const uint32_t from = stage + (at ^ (i << 5));
+      ldmatrix4<false, 0>(from, r[0]);
+      if constexpr (N > 1) ldmatrix4<false, STEP>(from, r[1]);
+      if constexpr (N > 2) ldmatrix4<false, 2 * STEP>(from, r[2]);
+      if constexpr (N > 3) ldmatrix4<false, 3 * STEP>(from, r[3]);
+      if constexpr (!E4M3) {
 #pragma unroll
-        for (int j = 0; j < (kChunks > 1 ? 2 : 1); ++j) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x4(r[2 * j], a0, a2);
-          e4m3x4_to_f16x4(r[2 * j + 1], a1, a3);
-          mma16816<true>(s, a0, a1, a2, a3, q[4 * i + 2 * j], q[4 * i + 2 * j + 1]);
-        }
+        for (int t = 0; t < N; ++t)
+          mma16816<false>(s[t], r[t][0], r[t][1], r[t][2], r[t][3], q[2 * i], q[2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < (kChunks > 1 ? 2 : 1); ++j)
+#pragma unroll
+          for (int t = 0; t < N; ++t) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(r[t][2 * j], a0, a2);
+            e4m3x4_to_f16x4(r[t][2 * j + 1], a1, a3);
+            mma16816<true>(s[t], a0, a1, a2, a3, q[4 * i + 2 * j], q[4 * i + 2 * j + 1]);
+          }
       }
     }
   }
@@ -328,15 +334,7 @@ struct Stage {
       }
     }
   }
-  // Of tile `tile` (a constant after unrolling), STEP bytes from one to the next.
-  template <int STEP>
-  static __device__ __forceinline__ void scores_of(int tile, uint32_t stage, uint32_t at,
-                                                   const uint32_t (&q)[D / 8], float (&s)[4]) {
-    if (tile == 0) scores<0>(stage, at, q, s);
-    if (tile == 1) scores<STEP>(stage, at, q, s);
-    if (tile == 2) scores<2 * STEP>(stage, at, q, s);
-    if (tile == 3) scores<3 * STEP>(stage, at, q, s);
-  }
+  // add() of tile `tile` (a constant after unrolling), STEP bytes from one to the next.
   template <int STEP>
   static __device__ __forceinline__ void add_of(int tile, uint32_t stage, uint32_t at, uint32_t p0,
                                                 uint32_t p1, float (&o)[D / 16][4]) {
@@ -688,13 +686,12 @@ __global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_
           vl = log_scale(shared_scale(stage, 1, true));
           if (w != 0.f) vl = fmaxf(vl, log_scale(shared_scale(stage, 1, false)));
         }
+        float s[4][4];      // of tokens 2 j and 2 j + 1
+        Y::template scores<4, 2 * Y::kRow>(stage, at, q, s);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {      // tokens 2 j and 2 j + 1
-          if (2 * j >= count) continue;    // uniform
-          float s[4];
-          Y::template scores_of<2 * Y::kRow>(j, stage, at, q, s);
-          if (c == j) y = mine ? fmaf(wb, s[3], wa * s[1]) : fmaf(wb, s[2], wa * s[0]);
-        }
+        for (int j = 0; j < 4; ++j)
+          if (c == j)
+            y = mine ? fmaf(wb, s[j][3], wa * s[j][1]) : fmaf(wb, s[j][2], wa * s[j][0]);
         y = cc <= at_pos ? fmaf(y, at_scale, at_beta) : -INFINITY;
         ps[st * 32] = y;
         top = fmaxf(top, y + vl);
@@ -721,11 +718,13 @@ __global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_
         for (int pair = 0; pair < NT; ++pair, ++k) {
           const bool second = FLAT ? t + STEP / 2 < count : pair * 16 + 8 < a.n_off;
           const uint32_t stage = take();
+          float both[2][4];      // (an absent second tile: not used)
+          Y::template scores<2, Y::kTile>(stage, at_k, q, both);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (i == 1 && !second) continue;
-            float s[4], va = 0.f, vc = 0.f, ka = 1.f, kc = 1.f;
-            Y::template scores_of<Y::kTile>(i, stage, at_k, q, s);
+            const float(&s)[4] = both[i];
+            float va = 0.f, vc = 0.f, ka = 1.f, kc = 1.f;
             if constexpr (E4M3) {
               ka = row_scale(stage, 0, i, 0);
               kc = row_scale(stage, 0, i, 1);
@@ -791,13 +790,13 @@ __global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_
       const bool second = t0 + 1 < t_past, more = t0 + t_step < t_past;
       float s[2][4], nm[2] = {-INFINITY, -INFINITY};
       uint32_t stage = take();
+      Y::template scores<2, Y::kTile>(stage, at_k, q, s);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (i == 1 && !second) {
           s[1][0] = s[1][1] = s[1][2] = s[1][3] = -INFINITY;
           continue;
         }
-        Y::template scores_of<Y::kTile>(i, stage, at_k, q, s[i]);
         const int t = t0 + i;
         float ka[2] = {scale[0], scale[1]}, kc[2] = {scale[0], scale[1]}, va = 0.f, vc = 0.f;
         if constexpr (E4M3) {
