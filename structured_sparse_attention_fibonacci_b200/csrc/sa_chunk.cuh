@@ -349,10 +349,18 @@ template <typename QT, int D, bool E4M3>
 __device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, int n, int b,
                                        int pos, bool inside);
 
-// Shared memory of a warp: two stages, and (interpolated distances) a score per lane of
-// every shared stage.
+// Bytes of a stage, and of a warp's shared memory: two stages, and (shared stages of
+// interpolated distances) a score per lane of each. Plain rows of 128 without shared
+// stages take 32 rows: the 8 KB per CTA are a fifth of what the L1 has left there
+// (16384 tokens, 32 heads over 4: 297 -> 274 us).
+template <int D, bool E4M3>
+__host__ __device__ __forceinline__ constexpr int stage_bytes(bool shared) {
+  return !E4M3 && D == 128 && !shared ? 32 * Stage<D, E4M3>::kRow : Stage<D, E4M3>::kBytes;
+}
 template <int D, bool E4M3, int NT, bool TEAM>
-constexpr int kWarpBytes = 2 * Stage<D, E4M3>::kBytes + (TEAM ? 0 : NT * 4 * 32 * 4);
+__host__ __device__ __forceinline__ constexpr int warp_bytes(bool shared) {
+  return 2 * stage_bytes<D, E4M3>(shared) + (!TEAM && shared ? NT * 4 * 32 * 4 : 0);
+}
 
 // A lane's walk over the pool rows that one member has for consecutive tokens:
 // mostly the next row of the same page.
@@ -421,7 +429,8 @@ __global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_
   float o[D / 16][4];
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  uint8_t* const own_smem = s_stages + warp * kWarpBytes<D, E4M3, NT, TEAM>;
+  const bool shares = a.shift == 3;      // 8 tokens of one head
+  uint8_t* const own_smem = s_stages + warp * warp_bytes<D, E4M3, NT, TEAM>(shares);
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(own_smem);
   const int hrow = h * a.pd.d, page_rows = a.Hkv * a.pd.d;
   // a team member's share: the last one has the offsets, the others every window_by-th
@@ -457,20 +466,20 @@ __global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_
     // values in turn; offset values ----
     const int own = Y::own();
     uint32_t in = ring, out = ring;
-    constexpr uint32_t kFlip = Y::kBytes;
+    const uint32_t flip_by = stage_bytes<D, E4M3>(shares);
     auto stage_in = [&](const uint8_t* rows, int row, bool two, bool keys) {
       Y::fill(in, own, rows, row, two);
       if constexpr (E4M3) {
         if (keys) copy4(in + Y::kScales + lane * 4, ks + row);
         copy4(in + Y::kScales + Y::kValues + lane * 4, vs + row);
       }
-      in = ring + kFlip - (in - ring);
+      in = ring + flip_by - (in - ring);
     };
     auto take = [&]() {      // the next stage to use, complete and visible to the warp
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncwarp();
       const uint32_t s = out;
-      out = ring + kFlip - (out - ring);
+      out = ring + flip_by - (out - ring);
       return s;
     };
     auto commit = []() { asm volatile("cp.async.commit_group;" ::: "memory"); };
@@ -532,7 +541,7 @@ __global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_
         copy4(at + Y::kValues, vs + row);
         if (lane < 4) copy4(at8 + Y::kValues, vs + row8);
       }
-      in = ring + kFlip - (in - ring);
+      in = ring + flip_by - (in - ring);
       ++next_st;
     };
     auto restart = [&]() {      // the values go over the same tokens again
@@ -666,7 +675,7 @@ __global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_
     // KIND 3: a lane has offset g % 4 of each stage for one token, 2c + mine. The loops
     // stay loops (four of them unrolled did not fit the instruction cache), so the
     // scores wait in shared memory.
-    [[maybe_unused]] float* const ps = reinterpret_cast<float*>(own_smem + 2 * Y::kBytes) + lane;
+    [[maybe_unused]] float* const ps = reinterpret_cast<float*>(own_smem + 2 * flip_by) + lane;
     [[maybe_unused]] const int mine = g >> 2;
     if constexpr (KIND == 3) {
       // ---- offset scores, rows shared by the tokens ----
@@ -972,7 +981,7 @@ __global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_
       run(std::integral_constant<int, 1>());
     } else if (!__all_sync(0xffffffffu, off_w == 0.f)) {
       if constexpr (!TEAM && NT > 0) {
-        if (a.shift == 3 && count > 3)
+        if (shares && count > 3)
           run(std::integral_constant<int, 3>());
         else
           run(std::integral_constant<int, 0>());
@@ -1017,7 +1026,7 @@ __global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_
   asm volatile("cp.async.wait_all;" ::: "memory");
   if constexpr (TEAM) {      // the first member joins the parts
     constexpr int kPart = D / 4 + 4;      // floats of a lane's part
-    static_assert(kPart * 32 * 4 <= 2 * Y::kBytes, "a part fits a warp's stages");
+    static_assert(kPart * 32 * 4 <= 2 * 32 * Y::kRow, "a part fits a warp's stages");
     float* mine = reinterpret_cast<float*>(own_smem) + lane;
     __syncwarp();
     if (warp > 0) {
@@ -1038,7 +1047,8 @@ __global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_
     __syncthreads();      // (the returns before are the same for the whole CTA)
     if (warp > 0) return;
     for (int w = 1; w < kWarps; ++w) {
-      const float* part = reinterpret_cast<const float*>(s_stages + w * kWarpBytes<D, E4M3, NT, TEAM>) + lane;
+      const float* part = reinterpret_cast<const float*>(
+                              s_stages + w * warp_bytes<D, E4M3, NT, TEAM>(shares)) + lane;
       lost = lost || __shfl_sync(0xffffffffu, part[(D / 4) * 32] != part[(D / 4) * 32], 0);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -1086,7 +1096,7 @@ __global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_
   // then 16 bytes a lane of consecutive head dims.
   constexpr int kOut = D * 2 + 16;
   uint8_t* const out = own_smem;
-  static_assert(8 * kOut <= 2 * Y::kBytes, "the output tile fits the stages");
+  static_assert(8 * kOut <= 2 * 32 * Y::kRow, "the output tile fits the stages");
   __syncwarp();
   const float bad = __int_as_float(0x7fc00000);
   const float inv0 = nan ? bad : 1.f / l[0], inv1 = nan ? bad : 1.f / l[1];
@@ -1324,7 +1334,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const __grid_constant
 template <int D, bool E4M3, int NT, bool TEAM>
 cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t st) {
   const dim3 grid(TEAM ? a.blocks : (a.blocks + kWarps - 1) / kWarps, a.Hkv * a.groups, a.L);
-  constexpr int smem = kWarps * kWarpBytes<D, E4M3, NT, TEAM>;
+  const int smem = kWarps * warp_bytes<D, E4M3, NT, TEAM>(a.shift == 3);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
         k_chunk_tc<D, E4M3, NT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
