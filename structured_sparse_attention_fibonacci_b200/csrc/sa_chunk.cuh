@@ -46,9 +46,10 @@
 // A masked probability is 0, and 0 * Inf or NaN is NaN: a block with a non-finite
 // output is computed again query by query (one_query), from its members alone.
 //
-// 32-bit queries (k_chunk_f32, one_query): one warp per (token, query head) on the
-// CUDA cores, chunks of 32 members: four lanes per member for the scores, lanes over
-// head dims for the values. 4096 tokens, 16 heads of 64, window 12: 180 us.
+// 32-bit queries (k_chunk_f32, one_query): one warp per token and up to 4 query heads of
+// a key/value head on the CUDA cores, chunks of 32 members: four lanes per member for
+// the scores, lanes over head dims for the values. 4096 tokens, 16 heads of 64, window
+// 12: 181 us; two groups of 8 of them: 176 us head by head, 91 in fours.
 #pragma once
 
 #include <type_traits>
@@ -1173,15 +1174,17 @@ __device__ __forceinline__ void load_part(const uint8_t* base, int D, int row, i
   }
 }
 
-// One query (token row n of sequence b at position pos, query head hq) by one
-// warp: members 32 at a time, and no row but its members' is touched.
-template <typename QT, int D, bool E4M3>
-__device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, int n, int b,
-                                       int pos, bool inside) {
+// NH query heads (from hq on, `live` of them) of one key/value head and one token (row n
+// of sequence b at position pos) by one warp: members 32 at a time, and no row but
+// their members' is touched.
+template <typename QT, int D, bool E4M3, int NH>
+__device__ __forceinline__ void query_heads(const ChunkArgs& a, int layer, int hq, int live, int n,
+                                            int b, int pos, bool inside) {
   constexpr bool BF16 = !E4M3 && sizeof(QT) == 2;
   constexpr int QE = D / 4;                        // elements of a row per quad lane
   constexpr int VE = D >= 32 ? D / 32 : 1;         // value elements per lane
   constexpr int SPLIT = D >= 32 ? 1 : 2;           // D = 16: two members at a time
+  constexpr int BATCH = NH == 1 || D == 128 ? 2 : 4;      // value rows whose loads are in flight
   const int lane = threadIdx.x & 31, part = lane & 3, mm = lane >> 2;
   const int h = hq / a.G;
 
@@ -1201,17 +1204,21 @@ __device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, in
   const uint8_t* kb = reinterpret_cast<const uint8_t*>(a.kc) + pool * D * kElt;
   const uint8_t* vb = reinterpret_cast<const uint8_t*>(a.vc) + pool * D * kElt;
 
-  float q[QE];
-  load_row<QT, QE>(reinterpret_cast<const QT*>(a.q) + layer * a.ql + n * a.qn + hq * a.qh +
-                       part * QE, q);
   const size_t at = ((size_t)layer * a.N + n) * a.Hq + hq;
-  const float beta = a.beta ? __ldg(a.beta + at) : 0.f;
+  float q[NH][QE], beta[NH], m[NH], l[NH], o[NH][VE];
+#pragma unroll
+  for (int j = 0; j < NH; ++j) {
+    const int jj = min(j, live - 1);      // idle heads repeat the last one
+    load_row<QT, QE>(reinterpret_cast<const QT*>(a.q) + layer * a.ql + n * a.qn +
+                         (hq + jj) * a.qh + part * QE, q[j]);
+    beta[j] = a.beta ? __ldg(a.beta + at + jj) : 0.f;
+    m[j] = -INFINITY;
+    l[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) o[j][i] = 0.f;
+  }
   const int nw = min(a.W, pos + 1), ns = min(a.S, pos + 1);
   const int total = ok ? nw + ns + a.n_off : 0;
-
-  float m = -INFINITY, l = 0.f, o[VE];
-#pragma unroll
-  for (int i = 0; i < VE; ++i) o[i] = 0.f;
   const int d0 = (D >= 32 ? lane : (lane & 15)) * VE;
 
   for (int m0 = 0; m0 < total; m0 += 32) {
@@ -1241,94 +1248,149 @@ __device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, in
       if (rb >= 0) { kc *= __ldg(a.ks + pool + rb); vc *= __ldg(a.vs + pool + rb); }
     }
     // scores: 8 members at a time, four lanes each
-    float s = -INFINITY;
+    float s[NH], p[NH];
+#pragma unroll
+    for (int j = 0; j < NH; ++j) s[j] = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int ia = __shfl_sync(0xffffffffu, ra, i * 8 + mm);
       const int ib = __shfl_sync(0xffffffffu, rb, i * 8 + mm);
       const float xa = __shfl_sync(0xffffffffu, ka, i * 8 + mm);
       const float xb = __shfl_sync(0xffffffffu, kc, i * 8 + mm);
-      float dot = 0.f;
-      if (ia >= 0) {
-        float x[QE];
-        load_part<E4M3, BF16, QE>(kb, D, ia, part * QE, x);
-        float t = 0.f;
+      float dot[NH];
 #pragma unroll
-        for (int e = 0; e < QE; ++e) t = fmaf(q[e], x[e], t);
-        dot = t * xa;
-      }
-      if (ib >= 0) {
-        float x[QE];
-        load_part<E4M3, BF16, QE>(kb, D, ib, part * QE, x);
-        float t = 0.f;
+      for (int j = 0; j < NH; ++j) dot[j] = 0.f;
 #pragma unroll
-        for (int e = 0; e < QE; ++e) t = fmaf(q[e], x[e], t);
-        dot = fmaf(t, xb, dot);
+      for (int row = 0; row < 2; ++row) {
+        const int at_row = row ? ib : ia;
+        if (at_row < 0) continue;
+        float x[QE];
+        load_part<E4M3, BF16, QE>(kb, D, at_row, part * QE, x);
+#pragma unroll
+        for (int j = 0; j < NH; ++j) {
+          float t = 0.f;
+#pragma unroll
+          for (int e = 0; e < QE; ++e) t = fmaf(q[j][e], x[e], t);
+          dot[j] = fmaf(t, row ? xb : xa, dot[j]);
+        }
       }
-      dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-      dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-      const float mine = __shfl_sync(0xffffffffu, dot, (lane & 7) * 4);
-      if ((lane >> 3) == i) s = mine;
+#pragma unroll
+      for (int j = 0; j < NH; ++j) {
+        dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], 1);
+        dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], 2);
+        const float mine = __shfl_sync(0xffffffffu, dot[j], (lane & 7) * 4);
+        if ((lane >> 3) == i) s[j] = mine;
+      }
     }
-    s = ra >= 0 ? (s * a.scale + (off ? beta : 0.f)) * kLog2e : -INFINITY;
-    float nm = s;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
-    nm = fmaxf(m, nm);
-    const float z = nm == -INFINITY ? 0.f : nm;
-    const float f = exp2f(m - z), p = exp2f(s - z);
-    m = nm;
-    l = l * f + p;
+    for (int j = 0; j < NH; ++j) {
+      s[j] = ra >= 0 ? (s[j] * a.scale + (off ? beta[j] : 0.f)) * kLog2e : -INFINITY;
+      float nm = s[j];
 #pragma unroll
-    for (int i = 0; i < VE; ++i) o[i] *= f;
-    va *= p;
-    vc *= p;
+      for (int d = 16; d >= 1; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
+      nm = fmaxf(m[j], nm);
+      const float z = nm == -INFINITY ? 0.f : nm;
+      const float f = exp2f(m[j] - z);
+      p[j] = exp2f(s[j] - z);
+      m[j] = nm;
+      l[j] = l[j] * f + p[j];
+#pragma unroll
+      for (int i = 0; i < VE; ++i) o[j][i] *= f;
+    }
+    // values: lanes over head dims; an interpolated value is formed once for all heads
+    if constexpr (NH == 1) {      // (the probability is part of the rows' weights)
+      va *= p[0];
+      vc *= p[0];
+    }
     const int here = min(32, total - m0);
-    for (int i = 0; i < here; i += SPLIT) {
-      const int src = i + (SPLIT == 2 ? lane >> 4 : 0);
-      const int ia = __shfl_sync(0xffffffffu, ra, src & 31);
-      const int ib = __shfl_sync(0xffffffffu, rb, src & 31);
-      const float xa = __shfl_sync(0xffffffffu, va, src & 31);
-      const float xb = __shfl_sync(0xffffffffu, vc, src & 31);
-      if (ia >= 0) {
-        float x[VE];
-        load_part<E4M3, BF16, VE>(vb, D, ia, d0, x);
+    for (int i0 = 0; i0 < here; i0 += BATCH * SPLIT) {
+      float xa[BATCH][VE], xb[BATCH][VE];
+      int src[BATCH];
+      bool ina[BATCH], inb[BATCH];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) o[e] = fmaf(xa, x[e], o[e]);
+      for (int u = 0; u < BATCH; ++u) {
+        src[u] = (i0 + u * SPLIT + (SPLIT == 2 ? lane >> 4 : 0)) & 31;
+        const int ia = __shfl_sync(0xffffffffu, ra, src[u]);
+        const int ib = __shfl_sync(0xffffffffu, rb, src[u]);
+        ina[u] = i0 + u * SPLIT < here && ia >= 0;
+        inb[u] = ina[u] && ib >= 0;
+        if (ina[u]) load_part<E4M3, BF16, VE>(vb, D, ia, d0, xa[u]);
+        if (inb[u]) load_part<E4M3, BF16, VE>(vb, D, ib, d0, xb[u]);
       }
-      if (ib >= 0) {
-        float x[VE];
-        load_part<E4M3, BF16, VE>(vb, D, ib, d0, x);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) o[e] = fmaf(xb, x[e], o[e]);
+      for (int u = 0; u < BATCH; ++u) {
+        const float ya = __shfl_sync(0xffffffffu, va, src[u]);
+        const float yb = __shfl_sync(0xffffffffu, vc, src[u]);
+        if (inb[u]) {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) xa[u][e] = fmaf(yb, xb[u][e], ya * xa[u][e]);
+        } else if (ina[u]) {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) xa[u][e] *= ya;
+        }
+#pragma unroll
+        for (int j = 0; j < NH; ++j) {
+          const float pj = NH == 1 ? 1.f : __shfl_sync(0xffffffffu, p[j], src[u]);
+          if (ina[u]) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) o[j][e] = fmaf(pj, xa[u][e], o[j][e]);
+          }
+        }
       }
     }
   }
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  if constexpr (SPLIT == 2) o[0] += __shfl_xor_sync(0xffffffffu, o[0], 16);
   const bool nan = __any_sync(0xffffffffu, lost) || !ok;
   const float bad = __int_as_float(0x7fc00000);
-  const float inv = nan ? bad : 1.f / l;
-  if (D >= 32 || lane < 16) {
 #pragma unroll
-    for (int e = 0; e < VE; ++e) o[e] *= inv;
-    store_row<QT, VE>(reinterpret_cast<QT*>(a.o) + at * D + d0, o);
+  for (int j = 0; j < NH; ++j) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
+    if constexpr (SPLIT == 2) o[j][0] += __shfl_xor_sync(0xffffffffu, o[j][0], 16);
+    if (j >= live) continue;
+    const float inv = nan ? bad : 1.f / l[j];
+    if (D >= 32 || lane < 16) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) o[j][e] *= inv;
+      store_row<QT, VE>(reinterpret_cast<QT*>(a.o) + (at + j) * D + d0, o[j]);
+    }
+    if (lane == 0 && a.lse) a.lse[at + j] = nan ? bad : kLn2 * m[j] + logf(l[j]);
   }
-  if (lane == 0 && a.lse) a.lse[at] = nan ? bad : kLn2 * m + logf(l);
   if (lost) atomicOr(&g_chunk_err, kErrPage);
 }
 
-template <int D, bool E4M3>
+// One query out of a block of k_chunk_tc.
+template <typename QT, int D, bool E4M3>
+__device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, int n, int b,
+                                       int pos, bool inside) {
+  query_heads<QT, D, E4M3, 1>(a, layer, hq, 1, n, b, pos, inside);
+}
+
+template <int D, bool E4M3, int NH>
 __global__ void __launch_bounds__(kWarps * 32) k_chunk_f32(const __grid_constant__ ChunkArgs a) {
   const int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (n >= a.N) return;
+  const int per = (a.G + NH - 1) / NH;      // groups of NH heads per key/value head
+  const int h = blockIdx.y / per, j = (blockIdx.y % per) * NH;
   const int b = find_sequence(a.cu, a.B, 0, n);
   const int first = __ldg(a.cu + b);
   if (first < 0 || n < first || n >= __ldg(a.cu + b + 1)) return;
   const long long posl = (long long)__ldg(a.cached + b) + (n - first);
   const bool inside = posl >= 0 && posl < (long long)a.max_pages * a.pd.d;
-  one_query<float, D, E4M3>(a, blockIdx.z, blockIdx.y, n, b, inside ? (int)posl : 0, inside);
+  query_heads<float, D, E4M3, NH>(a, blockIdx.z, h * a.G + j, min(NH, a.G - j), n, b,
+                                  inside ? (int)posl : 0, inside);
+}
+
+// Heads of a group by one warp: a row is loaded once for all of them; as many as the
+// registers hold (4, at D = 128 2) where warps enough remain for 16 per SM.
+template <int D, bool E4M3, int NH>
+cudaError_t launch_f32(const ChunkArgs& a, cudaStream_t st) {
+  const long long warps = (long long)a.N * a.Hkv * ((a.G + NH - 1) / NH) * a.L;
+  if constexpr (NH > 1) {
+    if (a.G < NH || warps < 148 * 16) return launch_f32<D, E4M3, NH / 2>(a, st);
+  }
+  const dim3 grid((a.N + kWarps - 1) / kWarps, a.Hkv * ((a.G + NH - 1) / NH), a.L);
+  k_chunk_f32<D, E4M3, NH><<<grid, kWarps * 32, 0, st>>>(a);
+  return cudaSuccess;
 }
 
 template <int D, bool E4M3, int NT, bool TEAM>
@@ -1354,8 +1416,7 @@ cudaError_t launch_t(const ChunkArgs& a, bool f32, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   trace_mark("chunk_attn", st, true);
   if (f32) {
-    const dim3 grid((a.N + kWarps - 1) / kWarps, a.Hq, a.L);
-    k_chunk_f32<D, E4M3><<<grid, kWarps * 32, 0, st>>>(a);
+    e = launch_f32<D, E4M3, D == 128 ? 2 : 4>(a, st);
   } else {
     e = a.n_off == 0    ? launch_nt<D, E4M3, 0>(a, st)
         : a.n_off <= 16 ? launch_nt<D, E4M3, 1>(a, st)
