@@ -83,6 +83,12 @@ _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+def _int32(x):
+    """x, or the C int nearest to it, which means the same (a window past every row)
+    or is refused like it; ctypes would cut its upper bits off."""
+    return max(-(1 << 31), min(int(x), (1 << 31) - 1))
+
+
 def _empty_like(t):
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
@@ -104,15 +110,18 @@ def _on_its_device(call):
     """Runs call(first, ..., stream=) with the device of its first tensor current
     and stream (of that device) its current stream: allocations and launches go there."""
     @functools.wraps(call)
-    def wrapped(first, *args, stream=None, **kw):
+    def wrapped(*args, stream=None, **kw):
+        first = args[0] if args else kw.get("q", kw.get("cache"))
         t = first.k if isinstance(first, PagedCache) else first
+        if t is None:
+            return call(*args, **kw)      # which says what is missing
         index = t.get_device()
         if index < 0:
             raise ValueError("the tensors must be on a CUDA device")
         if stream is None and _current_device() == index:
-            return call(first, *args, **kw)
+            return call(*args, **kw)
         with _entered(index, stream):
-            return call(first, *args, **kw)
+            return call(*args, **kw)
     return wrapped
 
 
@@ -184,7 +193,7 @@ def _norm_args(q, k, q_weight, k_weight, eps, rotate, rope_base, pos0):
         _whole("k_weight", k_weight, (L_, D), torch.float32, dev)
     elif not rotate:
         raise ValueError("without weights there is only the rotation")
-    p = QkNormParams(L_, B, Hq, Hkv, T, D, int(pos0), int(bool(rotate)), float(eps),
+    p = QkNormParams(L_, B, Hq, Hkv, _int32(T), D, _int32(pos0), int(bool(rotate)), float(eps),
                      float(rope_base), _DTYPES[q.dtype])
     return dev, p, qs, ks
 
@@ -279,6 +288,8 @@ def _paged_args(cache, page_table, dtype, L_, N, Hq):
         raise ValueError("page_table must be [B, max_pages]")
     B, max_pages = page_table.shape
     _whole("page_table", page_table, (B, max_pages), torch.int32, dev)
+    if max(N, B, n_pages, page_size, max_pages) >= 1 << 31:
+        raise ValueError("every size must fit 32 bits")
     p = PagedParams(L_, N, B, Hkv if Hq is None else Hq, Hkv, D, n_pages, page_size, max_pages,
                     _DTYPES[dtype], SA_CACHE_E4M3 if quantised else SA_CACHE_PLAIN)
     c = Pages(k.data_ptr(), v.data_ptr(), _addr(k_scale), _addr(v_scale), page_table.data_ptr())
@@ -326,8 +337,8 @@ def cache_append(q, k, v, cache, page_table, cu_q, cached, *, q_weight=None, k_w
     _check("sparse_attn_cache_append",
            lib().sparse_attn_cache_append(
                p, c, cu_q.data_ptr(), cached.data_ptr(), q.data_ptr(), qs, k.data_ptr(), ks,
-               v.data_ptr(), vs, _addr(q_weight), _addr(k_weight), eps, rope_base,
-               q_out.data_ptr(), _raw_stream(dev)))
+               v.data_ptr(), vs, _addr(q_weight), _addr(k_weight), float(eps),
+               float(rope_base), q_out.data_ptr(), _raw_stream(dev)))
     return q_out
 
 
@@ -344,7 +355,7 @@ def cache_read(cache, page_table, lengths, *, rows=None, dtype=None, k_out=None,
         dtype = torch.bfloat16 if cache.k.dtype == torch.float8_e4m3fn else cache.k.dtype
     dev, p, c = _paged_args(cache, page_table, dtype, None, 0, None)
     _whole("lengths", lengths, (p.B,), torch.int32, dev)
-    rows = p.max_pages * p.page_size if rows is None else int(rows)
+    rows = p.max_pages * p.page_size if rows is None else _int32(rows)
     if rows < 0:
         raise ValueError("k_out and v_out must be [L, B, Hkv, rows, D], rows at least 0")
     shape = (p.L, p.B, p.Hkv, rows, p.D)
@@ -396,15 +407,19 @@ def chunk_attn(q, cache, page_table, cu_q, cached, alpha, *, window, offsets=FIB
     offs = _offsets(tuple(offsets))
     _check("sparse_attn_chunk",
            lib().sparse_attn_chunk(p, c, cu_q.data_ptr(), cached.data_ptr(), q.data_ptr(), qs,
-                                   alpha.data_ptr(), _addr(beta), window, len(offs), offs, sinks,
-                                   scale, out.data_ptr(), _addr(lse), _raw_stream(dev)))
+                                   alpha.data_ptr(), _addr(beta), _int32(window), len(offs),
+                                   offs, _int32(sinks), float(scale), out.data_ptr(), _addr(lse),
+                                   _raw_stream(dev)))
     return out, lse
 
 
 @functools.lru_cache(maxsize=64)
 def _offsets(offsets):
     """The offset table as a C array (copied by the library during the call)."""
-    return (ctypes.c_int32 * len(offsets))(*[int(x) for x in offsets])
+    offsets = [int(x) for x in offsets]
+    if any(x != _int32(x) for x in offsets):
+        raise ValueError("offsets must fit 32 bits")
+    return (ctypes.c_int32 * len(offsets))(*offsets)
 
 
 def _bind(L):

@@ -635,3 +635,34 @@ def test_a_query_of_nan_or_infinities_stays_alone(dtype, fmt):
     # of the exact one, for |O| <= A <= 3)
     assert ((out[0][~spoiled].float() - good[0][~spoiled].float()).abs() <= 0.05).all()
     assert torch.isfinite(lse[0][~spoiled]).all()
+
+
+def test_calls_by_keyword_and_with_other_numbers():
+    import numpy as np
+    t = plain.Batch(1, 1, 32, 16, [5], [6], BF, "plain", seed=1)
+    cache, table, cu, cached = t.device(sa)
+    q = torch.randn((1, 6, 1, 32), generator=torch.Generator().manual_seed(0)).to(BF).to(DEV)
+    alpha = torch.ones(1, device=DEV)
+    a = sa.chunk_attn(q, cache, table, cu, cached, alpha, window=4, sinks=1)
+    b = sa.chunk_attn(q=q, cache=cache, page_table=table, cu_q=cu, cached=cached, alpha=alpha,
+                      window=np.int64(4), sinks=np.int32(1), offsets=np.array(FIB), scale=np.float32(0))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # windows past 32 bits are windows past every row; other numbers there are refused
+    wide = sa.chunk_attn(q, cache, table, cu, cached, alpha, window=100)
+    for window in (1 << 31, 1 << 32, (1 << 32) + 3):
+        x = sa.chunk_attn(q, cache, table, cu, cached, alpha, window=window)
+        assert torch.equal(x[0], wide[0]) and torch.equal(x[1], wide[1])
+    for kw in (dict(window=-(1 << 32) + 4), dict(window=4, sinks=-(1 << 32)),
+               dict(window=4, sinks=1 << 32)):
+        with pytest.raises(sa.SparseAttnError):
+            sa.chunk_attn(q, cache, table, cu, cached, alpha, **kw)
+    for offset in ((1 << 32) + 3, -(1 << 32) + 3):
+        with pytest.raises(ValueError):
+            sa.chunk_attn(q, cache, table, cu, cached, alpha, window=4, offsets=(2, offset))
+    k, v = sa.cache_read(cache=cache, page_table=table,
+                         lengths=torch.tensor([11], dtype=torch.int32, device=DEV))
+    assert torch.equal(k, sa.cache_read(cache, table, cached + 6)[0]) and bool(k[..., :11, :].any())
+    with pytest.raises(TypeError):
+        sa.chunk_attn(cache=cache)
+    with pytest.raises(TypeError):
+        sa.chunk_attn()
