@@ -259,6 +259,9 @@ sa_status sparse_attn_decode_prior(const sa_params* p, int32_t pos, const void* 
  *       aligned; one call's at a time (calls that may overlap, captured graphs
  *       among them, need one each). 0 bytes without weights.
  * B = 0 or T = 0 is a call without rows: it writes zero weight gradients.
+ * The first call with a head dim, a rope_base and more positions than before makes
+ * a table of cosines on the device (kept, as the forward's) and waits for it: under
+ * stream capture such a call is refused with SA_ERR_CUDA, and the capture goes on.
  */
 typedef struct {
   int64_t layer, batch, head, row; /* distances in elements */
@@ -349,7 +352,8 @@ typedef struct {
  * 16-byte aligned, both or neither) queries and keys are normed first, as in
  * sparse_attn_qk_norm_rope. q, k, v: rows [L][N][heads][D] of any strides that
  * are multiples of 16 bytes (slices of one projection's output), 16-byte aligned;
- * q_out: contiguous [L][N][Hq][D], not overlapping them.
+ * q_out: contiguous [L][N][Hq][D], not overlapping them. The table of cosines is as
+ * long as the page table reaches, so one call before a capture suffices.
  */
 sa_status sparse_attn_cache_append(const sa_paged_params* p, const sa_pages* pages,
                                    const int32_t* cu_q, const int32_t* cached, const void* q,

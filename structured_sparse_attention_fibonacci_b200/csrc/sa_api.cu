@@ -70,7 +70,13 @@ sa_status rope_table(int T, int D, float base, cudaStream_t st, const float2** o
   int cap = 4096;
   while (cap < T) cap *= 2;
   float2* ptr = nullptr;
-  if (cudaMalloc(&ptr, (size_t)cap * (D / 2) * sizeof(float2)) != cudaSuccess) return SA_ERR_CUDA;
+  cudaStreamCaptureStatus capture;      // (an allocation would end it)
+  if (cudaStreamIsCapturing(st, &capture) != cudaSuccess ||
+      capture != cudaStreamCaptureStatusNone ||
+      cudaMalloc(&ptr, (size_t)cap * (D / 2) * sizeof(float2)) != cudaSuccess) {
+    cudaGetLastError();      // reported here: later calls do not fail for it
+    return SA_ERR_CUDA;
+  }
   if (sa::launch_rope_table(ptr, cap, D, (double)base, st) != cudaSuccess ||
       cudaStreamSynchronize(st) != cudaSuccess) {
     cudaFree(ptr);

@@ -186,3 +186,26 @@ def test_backward_replays_from_graphs_with_their_own_workspaces():
     for (_, out), s in zip(graphs, sets):
         for a, b in zip(out, s[5]):
             assert torch.equal(a, b)
+
+
+def test_a_capture_that_needs_a_new_table_is_refused_and_goes_on():
+    q, k = (torch.randn(1, 1, 2, 9, 32, device=DEV) for _ in range(2))
+    base = 4321.0      # used nowhere else
+    out = torch.zeros_like(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        with pytest.raises(sa.SparseAttnError):
+            sa.qk_norm_rope(q, k, None, None, rope_base=base)
+        out.copy_(q)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, q)
+    want = sa.qk_norm_rope(q, k, None, None, rope_base=base)[0]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        sa.qk_norm_rope(q, k, None, None, rope_base=base, q_out=out, k_out=torch.empty_like(k))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
