@@ -11,7 +11,8 @@ present, the calls raise.
     dq, dk, dv, dalpha = bwd(q, k, v, O, lse, dO, alpha, window=12)
 
 ``paged.py`` binds the query/key norm, the paged cache and the attention over
-it (qk_norm_rope, cache_append, cache_read, chunk_attn).
+it (qk_norm_rope, cache_append, cache_read, chunk_attn) through an extension
+module, since their smallest calls are shorter than ctypes takes.
 
 Method: "Depth-Staggered Fibonacci Spacing for Sparse Attention" (C. A.
 Capps), technical summary, Methodology -- "Attended set", "Scaling",

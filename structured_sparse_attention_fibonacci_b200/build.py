@@ -12,13 +12,16 @@ binding loads with ctypes:
                             staging round against the ring's size; a violation
                             sets bit 1 of the device error word (no trap), so
                             the parity tests can run under it in place of a
-                            memory checker.
+                            memory checker;
+and csrc/sa_binding.cpp with nvcc's host compiler, against the installed torch:
+  _binding.so               extension module behind paged.py's calls.
 """
 import concurrent.futures as cf
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -26,6 +29,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsparse_attn.so")
 LIB_BOUNDS = os.path.join(HERE, "libsparse_attn_bounds.so")
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "sa_binding.cpp")
 OBJ_DIR = os.path.join(HERE, "_build")
 
 NVCC_FLAGS = [
@@ -46,6 +51,9 @@ def _stale(lib):
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
+    if lib == BINDING:
+        deps = (BINDING_SRC, os.path.join(INCLUDE, "sparse_attn.h"), os.path.abspath(__file__))
+        return any(os.path.getmtime(d) > t for d in deps)
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     deps += glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
@@ -59,15 +67,36 @@ def _compile(nvcc, src, obj, extra, verbose):
     return obj
 
 
+def _build_binding(nvcc, verbose):
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-O2", "-std=c++17", "-shared",
+           "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_path("include"), "-I", INCLUDE, BINDING_SRC,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-cudart", "none", "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra=(), variants=None) -> str:
     """Compile the stale libraries (all with force); returns the main library's path."""
     nvcc = os.environ.get("NVCC", "nvcc")
     todo = [lib for lib in (variants or VARIANTS) if force or _stale(lib)]
-    if not todo:
+    binding = force or _stale(BINDING)
+    if not todo and not binding:
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     jobs = []
     with cf.ThreadPoolExecutor(max_workers=max(1, min(16, os.cpu_count() or 1))) as ex:
+        if binding:
+            jobs.append(ex.submit(_build_binding, nvcc, verbose))
         for lib in todo:
             tag = os.path.splitext(os.path.basename(lib))[0]
             objs = []
