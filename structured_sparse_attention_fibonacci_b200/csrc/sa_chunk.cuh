@@ -155,8 +155,11 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t& lo, uin
       : "r"(four));
 }
 
+// Past the L1: its data path is half of what the kernel waits for, and a row that passes
+// through it crosses it twice (16384 tokens, 16 heads of 64: window 64 162 -> 142 us,
+// interpolated, window 12 196 -> 168; 8 heads of 128: 203 -> 159).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -373,8 +376,18 @@ struct Walk {
 // NT: pairs of offset tiles (16 offsets each), 0 .. 2. TEAM: the CTA's warps share one
 // block (an instance of its own: the shares cost the others 4 %). Two stages per warp are in
 // flight: one more costs the L1 more than it hides (20 warps of 8 KB leave it 68 KB).
+// CTAs per SM, and with them the registers (96 a thread for five): more warps hide more
+// of the latency until the spills cost as much. 16384 tokens, plain rows: 16 heads of 64,
+// window 64 142 us with four, 136 with five; 32 heads of 128 over 4 258 with four, 241
+// with three; 16 heads of 16 102 with six, 117 with eight. e4m3 rows of 128: 219 with
+// four, 247 with three.
+template <int D, bool E4M3>
+__host__ __device__ __forceinline__ constexpr int chunk_ctas() {
+  return D == 128 ? (E4M3 ? 4 : 3) : D == 64 ? 5 : 6;
+}
 template <int D, bool E4M3, int NT, bool TEAM>
-__global__ void __launch_bounds__(kWarps * 32, D >= 64 ? 4 : D == 32 ? 5 : 6) k_chunk_tc(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3>())
+    k_chunk_tc(const __grid_constant__ ChunkArgs a) {
   using Y = Stage<D, E4M3>;
   extern __shared__ __align__(1024) uint8_t s_stages[];
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
