@@ -17,8 +17,9 @@
 // every head of the token; the norm and the 8-bit maximum cost log2(D/16)
 // shuffles. A decode step has few tokens: the rows are then split over
 // `parts` warps per token. Measured for 5446 tokens x 4 layers of 32 + 8 heads of
-// 128 into e4m3: 491 MB in about 100 us, 4.9 TB/s of 6.55; half the issue slots go
-// to the norm, the rotation and the conversions.
+// 128 into e4m3: 491 MB in 91 us, 5.4 TB/s of 6.55; 16384 tokens x 4 layers of 8 + 8
+// heads of 64: 82 us. Half the issue slots go to the norm, the rotation and the
+// conversions.
 #include "sa_paged.cuh"
 
 namespace sa {
@@ -41,34 +42,40 @@ struct AppendArgs {
   void* q_out; void* kc; void* vc; float* ks; float* vs;
 };
 
-// 16 elements of a row as they lie in memory: 8 from p, 8 from p + half.
+// A thread's copies in flight: its own 16 elements of the next rows, as 16-byte chunks
+// in slots of shared memory that no other thread touches (so no barrier is needed).
+// (Two rows a thread in registers, beside the 60 that the arithmetic takes, and five CTAs
+// per SM: 103 us where this takes 91; four stages 94, seven CTAs 99, eight 115: spills.)
 template <typename T>
-struct Raw {
-  static constexpr int kChunks = sizeof(T) / 2;      // 16-byte chunks of 8 elements
-  uint4 u[2][kChunks];
-  __device__ __forceinline__ void load(const T* p, int half) {
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      u[0][c] = __ldg(reinterpret_cast<const uint4*>(p) + c);
-      u[1][c] = __ldg(reinterpret_cast<const uint4*>(p + half) + c);
-    }
+struct Ahead {
+  static constexpr int kChunks = sizeof(T);      // 8 elements from j0, 8 from j0 + D / 2
+  static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;
+  static constexpr int kStage = kChunks * kAppendWarps * 32 * 16;
+  // (fp32: half a sector at a time, so through the L1)
+  static __device__ __forceinline__ void copy(uint32_t dst, const T* src) {
+    if constexpr (sizeof(T) == 2)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   }
-  __device__ __forceinline__ void get(int i, float (&x)[8]) const {
+};
+template <typename T>
+__device__ __forceinline__ void read8(const uint8_t* slot, float (&x)[8]) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const uint32_t w[4] = {u[i][c].x, u[i][c].y, u[i][c].z, u[i][c].w};
+  for (int c = 0; c < (int)sizeof(T) / 2; ++c) {
+    const uint4 u = *reinterpret_cast<const uint4*>(slot + c * kAppendWarps * 32 * 16);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 4) {
-          x[4 * c + e] = __uint_as_float(w[e]);
-        } else {
-          x[2 * e] = bf16lo(w[e]);
-          x[2 * e + 1] = bf16hi(w[e]);
-        }
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (sizeof(T) == 4) {
+        x[4 * c + e] = __uint_as_float(w[e]);
+      } else {
+        x[2 * e] = bf16lo(w[e]);
+        x[2 * e + 1] = bf16hi(w[e]);
       }
     }
   }
-};
+}
 
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
@@ -84,8 +91,10 @@ __device__ __forceinline__ float group_max(float v) {
 }
 
 template <typename T, int D, bool E4M3, bool NORM>
-__global__ void __launch_bounds__(kAppendWarps * 32, 5) k_cache_append(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 6) k_cache_append(const AppendArgs a) {
   constexpr int LANES = D / 16, ROWS = 32 / LANES, HALF = D / 2;
+  using Y = Ahead<T>;
+  __shared__ __align__(16) uint8_t s_ring[Y::kStages * Y::kStage];
   const int lane = threadIdx.x & 31, sub = lane % LANES, grp = lane / LANES;
   const long long wid = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   const int layer = blockIdx.y;
@@ -98,26 +107,32 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 5) k_cache_append(const App
   const T* v = reinterpret_cast<const T*>(a.v) + layer * a.vl + n * a.vn + j0;
   // Rows in turn: q heads, k heads, v heads. Every group of the warp takes part in
   // the shuffles; one without a row takes the last one again and does not store it.
-  // kBatch rows' loads are in flight at a time, the first ones before the sequence
-  // is known.
-  constexpr int kBatch = sizeof(T) == 2 ? 2 : 1;
-  Raw<T> raw[kBatch];
-  auto fetch_rows = [&](int r0) {
+  int next = part * ROWS, slot_in = 0, slot = 0;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(s_ring) + threadIdx.x * 16;
+  auto issue = [&]() {
+    if (next < rows) {
+      const int r = min(next + grp, rows - 1);
+      const T* from = r < a.Hq           ? q + r * a.qh
+                      : r < a.Hq + a.Hkv ? k + (r - a.Hq) * a.kh
+                                         : v + (r - a.Hq - a.Hkv) * a.vh;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = min(r0 + i * stride + grp, rows - 1);
-      if (r0 + i * stride < rows)      // uniform
-        raw[i].load(r < a.Hq           ? q + r * a.qh
-                    : r < a.Hq + a.Hkv ? k + (r - a.Hq) * a.kh
-                                       : v + (r - a.Hq - a.Hkv) * a.vh,
-                    HALF);
+      for (int c = 0; c < Y::kChunks; ++c)
+        Y::copy(mine + slot_in + c * kAppendWarps * 32 * 16,
+                from + c / (Y::kChunks / 2) * HALF + c % (Y::kChunks / 2) * (16 / (int)sizeof(T)));
+      next += stride;
+      slot_in = slot_in + Y::kStage == Y::kStages * Y::kStage ? 0 : slot_in + Y::kStage;
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  fetch_rows(part * ROWS);
+#pragma unroll
+  for (int i = 0; i < Y::kStages - 1; ++i) issue();      // before the sequence is known
 
   const int b = find_sequence(a.cu, a.B, 0, n);
   const int first = __ldg(a.cu + b);
-  if (n < first || n >= __ldg(a.cu + b + 1)) return;      // a row behind the last sequence
+  if (n < first || n >= __ldg(a.cu + b + 1)) {      // a row behind the last sequence
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
   const long long pos = (long long)__ldg(a.cached + b) + (n - first);
   const bool inside = pos >= 0 && pos < (long long)a.max_pages * a.pd.d;
   int page = -1, lp = 0;
@@ -135,114 +150,73 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 5) k_cache_append(const App
 #pragma unroll
     for (int i = 0; i < 8; ++i) cs[i] = make_float2(__int_as_float(0x7fc00000), 0.f);
   }
-  const int slot = (int)pos - lp * a.pd.d;
-  int base = part * ROWS;
-
-  // Batches of query heads alone, most of the work with grouped heads: nothing to
-  // choose per row, and the weights stay in registers.
-  if (base + (kBatch - 1) * stride + ROWS <= a.Hq) {
-    float w1[8], w2[8];
+  const int row_slot = (int)pos - lp * a.pd.d;
+  float w1[8], w2[8];
+  int weights_of = -1;
+#pragma unroll 1
+  for (int r0 = part * ROWS; r0 < rows; r0 += stride) {
+    issue();
+    asm volatile("cp.async.wait_group %0;" ::"n"(Y::kStages - 1) : "memory");
+    const uint8_t* from = s_ring + slot + threadIdx.x * 16;
+    slot = slot + Y::kStage == Y::kStages * Y::kStage ? 0 : slot + Y::kStage;
+    const bool live = r0 + grp < rows;
+    const int r = min(r0 + grp, rows - 1);
+    const int what = r < a.Hq ? 0 : (r < a.Hq + a.Hkv ? 1 : 2);       // q, k, v
+    float x1[8], x2[8];
+    read8<T>(from, x1);
+    read8<T>(from + Y::kStage / 2, x2);
     if constexpr (NORM) {
-      load_row<float, 8>(a.qw + (size_t)layer * D + j0, w1);
-      load_row<float, 8>(a.qw + (size_t)layer * D + j0 + HALF, w2);
-    }
-    T* dst = reinterpret_cast<T*>(a.q_out) + (((size_t)layer * a.N + n) * a.Hq + grp) * D + j0;
-    const T* src = q + grp * a.qh;
-    for (;;) {
+      float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        float x1[8], x2[8];
-        raw[i].get(0, x1);
-        raw[i].get(1, x2);
-        if constexpr (NORM) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x1[e], x1[e], fmaf(x2[e], x2[e], ss));
-          const float rstd = inverse_sqrt(group_sum<LANES>(ss) * (1.f / D) + a.eps);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x1[e] = x1[e] * rstd * w1[e];
-            x2[e] = x2[e] * rstd * w2[e];
-          }
-        }
-        rope_fwd<8>(x1, x2, cs);
-        T* to = dst + (size_t)(base + i * stride) * D;
-        store_row<T, 8>(to, x1);
-        store_row<T, 8>(to + HALF, x2);
-      }
-      base += kBatch * stride;
-      if (base + (kBatch - 1) * stride + ROWS > a.Hq) break;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) raw[i].load(src + (base + i * stride) * a.qh, HALF);
-    }
-    if (base < rows) fetch_rows(base);
-  }
-
-  for (bool first_batch = true; base < rows; base += kBatch * stride, first_batch = false) {
-    if (!first_batch) fetch_rows(base);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r0 = base + i * stride;
-      if (r0 >= rows) continue;      // uniform
-      const bool live = r0 + grp < rows;
-      const int r = min(r0 + grp, rows - 1);
-      const int what = r < a.Hq ? 0 : (r < a.Hq + a.Hkv ? 1 : 2);       // q, k, v
-      const int h = what == 0 ? r : (what == 1 ? r - a.Hq : r - a.Hq - a.Hkv);
-      float x1[8], x2[8];
-      raw[i].get(0, x1);
-      raw[i].get(1, x2);
-      if constexpr (NORM) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x1[i], x1[i], fmaf(x2[i], x2[i], ss));
-        ss = group_sum<LANES>(ss);
-        if (what < 2) {
+      for (int i = 0; i < 8; ++i) ss = fmaf(x1[i], x1[i], fmaf(x2[i], x2[i], ss));
+      ss = group_sum<LANES>(ss);
+      if (what < 2) {
+        if (weights_of != what) {
           const float* w = (what == 0 ? a.qw : a.kw) + (size_t)layer * D + j0;
-          float w1[8], w2[8];
           load_row<float, 8>(w, w1);
           load_row<float, 8>(w + HALF, w2);
-          const float rstd = inverse_sqrt(ss * (1.f / D) + a.eps);
+          weights_of = what;
+        }
+        const float rstd = inverse_sqrt(ss * (1.f / D) + a.eps);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x1[i] = x1[i] * rstd * w1[i];
-            x2[i] = x2[i] * rstd * w2[i];
-          }
+        for (int i = 0; i < 8; ++i) {
+          x1[i] = x1[i] * rstd * w1[i];
+          x2[i] = x2[i] * rstd * w2[i];
         }
       }
-      if (what < 2) rope_fwd<8>(x1, x2, cs);
-      if (what == 0) {
-        if (live) {
-          T* dst = reinterpret_cast<T*>(a.q_out) + (((size_t)layer * a.N + n) * a.Hq + h) * D + j0;
-          store_row<T, 8>(dst, x1);
-          store_row<T, 8>(dst + HALF, x2);
-        }
-      }
-      if (r0 + ROWS <= a.Hq) continue;      // queries only (uniform)
-      float scale = 1.f;
+    }
+    if (what < 2) rope_fwd<8>(x1, x2, cs);
+    if (what == 0) {      // (a lane group without a row is never here: v rows are last)
+      T* dst = reinterpret_cast<T*>(a.q_out) + (((size_t)layer * a.N + n) * a.Hq + r) * D + j0;
+      store_row<T, 8>(dst, x1);
+      store_row<T, 8>(dst + HALF, x2);
+    }
+    if (r0 + ROWS <= a.Hq) continue;      // queries only (uniform)
+    float scale = 1.f;
+    if constexpr (E4M3) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max_nan(m, max_nan(fabsf(x1[i]), fabsf(x2[i])));
+      scale = e4m3_scale(group_max<LANES>(m));
+    }
+    if (what > 0 && live && have) {
+      const int h = what == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
+      const size_t row = (((size_t)layer * a.n_pages + page) * a.Hkv + h) * a.pd.d + row_slot;
       if constexpr (E4M3) {
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max_nan(m, max_nan(fabsf(x1[i]), fabsf(x2[i])));
-        scale = e4m3_scale(group_max<LANES>(m));
-      }
-      if (what > 0 && live && have) {
-        const size_t row = (((size_t)layer * a.n_pages + page) * a.Hkv + h) * a.pd.d + slot;
-        if constexpr (E4M3) {
-          const float inv = 1.f / scale;     // a power of two: exact
-          uint8_t* dst = reinterpret_cast<uint8_t*>(what == 1 ? a.kc : a.vc) + row * D + j0;
-          uint2 u;
-          u.x = float4_to_e4m3x4(x1[0] * inv, x1[1] * inv, x1[2] * inv, x1[3] * inv);
-          u.y = float4_to_e4m3x4(x1[4] * inv, x1[5] * inv, x1[6] * inv, x1[7] * inv);
-          *reinterpret_cast<uint2*>(dst) = u;
-          u.x = float4_to_e4m3x4(x2[0] * inv, x2[1] * inv, x2[2] * inv, x2[3] * inv);
-          u.y = float4_to_e4m3x4(x2[4] * inv, x2[5] * inv, x2[6] * inv, x2[7] * inv);
-          *reinterpret_cast<uint2*>(dst + HALF) = u;
-          if (sub == 0) (what == 1 ? a.ks : a.vs)[row] = scale;
-        } else {
-          T* dst = reinterpret_cast<T*>(what == 1 ? a.kc : a.vc) + row * D + j0;
-          store_row<T, 8>(dst, x1);
-          store_row<T, 8>(dst + HALF, x2);
-        }
+        const float inv = 1.f / scale;     // a power of two: exact
+        uint8_t* dst = reinterpret_cast<uint8_t*>(what == 1 ? a.kc : a.vc) + row * D + j0;
+        uint2 u;
+        u.x = float4_to_e4m3x4(x1[0] * inv, x1[1] * inv, x1[2] * inv, x1[3] * inv);
+        u.y = float4_to_e4m3x4(x1[4] * inv, x1[5] * inv, x1[6] * inv, x1[7] * inv);
+        *reinterpret_cast<uint2*>(dst) = u;
+        u.x = float4_to_e4m3x4(x2[0] * inv, x2[1] * inv, x2[2] * inv, x2[3] * inv);
+        u.y = float4_to_e4m3x4(x2[4] * inv, x2[5] * inv, x2[6] * inv, x2[7] * inv);
+        *reinterpret_cast<uint2*>(dst + HALF) = u;
+        if (sub == 0) (what == 1 ? a.ks : a.vs)[row] = scale;
+      } else {
+        T* dst = reinterpret_cast<T*>(what == 1 ? a.kc : a.vc) + row * D + j0;
+        store_row<T, 8>(dst, x1);
+        store_row<T, 8>(dst + HALF, x2);
       }
     }
   }
