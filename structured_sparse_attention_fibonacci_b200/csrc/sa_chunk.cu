@@ -1,5 +1,7 @@
 // Attention of a chunk of new tokens over the paged cache: choice of the kernel
 // instance. The kernels are in sa_chunk.cuh.
+#include <algorithm>
+
 #include "sa_chunk.cuh"
 
 namespace sa {
@@ -26,13 +28,21 @@ cudaError_t launch_chunk_attn(const PagedProblem& p, const PagedPtrs& c, const C
   a.shift = a.per == 1 ? 3 : (a.per == 2 ? 2 : (a.per <= 4 ? 1 : 0));
   a.blocks = a.shift ? (p.N >> a.shift) + p.B : p.N;
   const long long warps = (long long)a.blocks * a.Hkv * a.groups * a.L;
-  const long long rows = (long long)x.W + (1 << a.shift) - 1;
+  const long long rows = std::min((long long)x.W, (long long)p.max_pages * p.page_size) +
+                         (1 << a.shift) - 1;
   // Few blocks, as in a decode step, and a window of three tiles or more (the sinks
   // are one): a CTA's warps share a block while all CTAs are resident at once, four
-  // per SM (one token, 16 heads, window 64 with sinks: 8.9 -> 6.9 us; with a window
-  // of one pair of tiles the join costs what it saves).
-  a.team = (rows + 15) / 16 + (x.S > 0) >= 3 && warps <= 148 * 4;
+  // per SM, of plain rows of 128 three (one token, 16 heads, window 64 with sinks:
+  // 8.9 -> 6.9 us; with a window of one pair of tiles the join costs what it saves).
+  // Clusters of two, four or eight CTAs share it where each of their warps has more
+  // than four pairs left (window 1024: 14.2 us by one CTA, 8.9 by two; 4096: 40 by one,
+  // 12.7 by eight).
   const bool f32 = p.dtype == SA_DTYPE_F32, q8 = p.format == SA_CACHE_E4M3;
+  const long long tiles = (rows + 15) / 16 + (x.S > 0), pairs = (tiles + 1) / 2;
+  const long long room = 148 * (p.D == 128 && !q8 ? 3 : 4);
+  a.team = tiles >= 3 && warps <= room ? 1 : 0;
+  while (a.team > 0 && a.team < 8 && pairs > 4 * (4 * a.team - 1) && warps * a.team * 2 <= room)
+    a.team *= 2;
   switch (p.D) {
     case 16: return launch_chunk_of<16>(a, f32, q8, st);
     case 32: return launch_chunk_of<32>(a, f32, q8, st);

@@ -61,7 +61,7 @@ namespace sa {
 struct ChunkArgs {
   int L, N, B, Hq, Hkv, n_pages, max_pages, W, n_off, S, blocks;
   int G, groups, per, shift;      // heads per kv head; column groups, heads in one, log2 tokens
-  bool team;                      // a CTA's warps share a block
+  int team;                       // CTAs whose warps share a block; 0: a block per warp
   int inv_per;                    // ceil(256 / per): col * inv_per / 256 = col / per for col < 8
   FastDiv pd;
   float scale;
@@ -176,6 +176,32 @@ __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr), "n"(OFFSET)
                  : "memory");
+}
+// Clusters of CTAs: this one's rank, a barrier, the address of what p is in the CTA of
+// rank r, and a load from there.
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
+  asm volatile(
+      "barrier.cluster.arrive.release;\n\t"
+      "barrier.cluster.wait.acquire;" ::: "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ uint32_t cluster_address(const void* p, int r) {
+  uint32_t there;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(there)
+      : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(r));
+  return there;
+}
+__device__ __forceinline__ float load_cluster(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
 }
 __device__ __forceinline__ float load_shared(uint32_t addr) {
   float x;
@@ -373,26 +399,26 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------------------
-// NT: pairs of offset tiles (16 offsets each), 0 .. 2. TEAM: the CTA's warps share one
-// block (an instance of its own: the shares cost the others 4 %). Two stages per warp are in
-// flight: one more costs the L1 more than it hides (20 warps of 8 KB leave it 68 KB).
+// NT: pairs of offset tiles (16 offsets each), 0 .. 2. TEAM: the warps of a cluster of
+// a.team CTAs share one block (an instance of its own: the shares cost the others 4 %).
 // CTAs per SM, and with them the registers (96 a thread for five): more warps hide more
 // of the latency until the spills cost as much. 16384 tokens, plain rows: 16 heads of 64,
 // window 64 142 us with four, 136 with five; 32 heads of 128 over 4 258 with four, 241
 // with three; 16 heads of 16 102 with six, 117 with eight. e4m3 rows of 128: 219 with
-// four, 247 with three.
-template <int D, bool E4M3>
+// four, 247 with three. Of teams there are at most four per SM (one token, 16 heads of
+// 64, window 4096 by one CTA: 49 us with registers for five, 40 for four).
+template <int D, bool E4M3, bool TEAM>
 __host__ __device__ __forceinline__ constexpr int chunk_ctas() {
-  return D == 128 ? (E4M3 ? 4 : 3) : D == 64 ? 5 : 6;
+  return D == 128 ? (E4M3 ? 4 : 3) : TEAM ? 4 : D == 64 ? 5 : 6;
 }
 template <int D, bool E4M3, int NT, bool TEAM>
-__global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3>())
+__global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3, TEAM>())
     k_chunk_tc(const __grid_constant__ ChunkArgs a) {
   using Y = Stage<D, E4M3>;
   extern __shared__ __align__(1024) uint8_t s_stages[];
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int warp = threadIdx.x >> 5;
-  const int x = TEAM ? blockIdx.x : blockIdx.x * kWarps + warp;
+  const int x = TEAM ? blockIdx.x / a.team : blockIdx.x * kWarps + warp;
   if (x >= a.blocks) return;
   const int h = blockIdx.y / a.groups, grp = blockIdx.y % a.groups, layer = blockIdx.z;
 
@@ -449,9 +475,11 @@ __global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3>())
   const int hrow = h * a.pd.d, page_rows = a.Hkv * a.pd.d;
   // a team member's share: the last one has the offsets, the others every window_by-th
   // pair of window tiles from the window_at-th on (0: none)
-  const bool offsets = !TEAM || warp == kWarps - 1;
-  const int window_by = !TEAM ? 1 : NT == 0 ? kWarps : offsets ? 0 : kWarps - 1;
-  const int window_at = TEAM && window_by ? warp : 0;
+  const int members = TEAM ? kWarps * a.team : 1, rank = TEAM ? cluster_rank() : 0;
+  const int member = TEAM ? rank * kWarps + warp : 0;
+  const bool offsets = member == members - 1;
+  const int window_by = !TEAM ? 1 : NT == 0 ? members : offsets ? 0 : members - 1;
+  const int window_at = TEAM && window_by ? member : 0;
   int n_far = a.n_off;                   // offsets that have rows of their own
   unsigned near_lo = 0, near_hi = 0;     // distances 0..31 and 32..63 folded into the window
 
@@ -1038,12 +1066,12 @@ __global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3>())
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if constexpr (TEAM) {      // the first member joins the parts
+  if constexpr (TEAM) {      // each CTA's first member joins its parts, then the first CTA's these
     constexpr int kPart = D / 4 + 4;      // floats of a lane's part
     static_assert(kPart * 32 * 4 <= 2 * 32 * Y::kRow, "a part fits a warp's stages");
-    float* mine = reinterpret_cast<float*>(own_smem) + lane;
-    __syncwarp();
-    if (warp > 0) {
+    auto publish = [&]() {
+      float* mine = reinterpret_cast<float*>(own_smem) + lane;
+      __syncwarp();
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -1054,29 +1082,45 @@ __global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3>())
         mine[(D / 4 + 2 + e) * 32] = l[e];
       }
       if (__any_sync(0xffffffffu, lost) && lane == 0) {
-        mine[(D / 4) * 32] = __int_as_float(0x7fc00000);      // tells the first member
+        mine[(D / 4) * 32] = __int_as_float(0x7fc00000);      // tells who joins it
         atomicOr(&g_chunk_err, kErrPage);
       }
-    }
-    __syncthreads();      // (the returns before are the same for the whole CTA)
+    };
+    auto absorb = [&](auto part) {      // part(i): its float i
+      const bool theirs = __shfl_sync(0xffffffffu, part(D / 4) != part(D / 4), 0);
+      lost = lost || theirs;      // (every lane shuffles, lost or not)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mp = part(D / 4 + e), top = fmaxf(m[e], mp);
+        const float z = top == -INFINITY ? 0.f : top;
+        const float f = exp2_approx(m[e] - z), fp = exp2_approx(mp - z);
+        m[e] = top;
+        l[e] = l[e] * f + part(D / 4 + 2 + e) * fp;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          o[j][e] = o[j][e] * f + part(4 * j + e) * fp;
+          o[j][2 + e] = o[j][2 + e] * f + part(4 * j + 2 + e) * fp;
+        }
+      }
+    };
+    if (warp > 0) publish();
+    __syncthreads();      // (the returns before are the same for all of the team)
     if (warp > 0) return;
     for (int w = 1; w < kWarps; ++w) {
       const float* part = reinterpret_cast<const float*>(
                               s_stages + w * warp_bytes<D, E4M3, NT, TEAM>(shares)) + lane;
-      lost = lost || __shfl_sync(0xffffffffu, part[(D / 4) * 32] != part[(D / 4) * 32], 0);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float mp = part[(D / 4 + e) * 32], top = fmaxf(m[e], mp);
-        const float z = top == -INFINITY ? 0.f : top;
-        const float f = exp2_approx(m[e] - z), fp = exp2_approx(mp - z);
-        m[e] = top;
-        l[e] = l[e] * f + part[(D / 4 + 2 + e) * 32] * fp;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          o[j][e] = o[j][e] * f + part[(4 * j + e) * 32] * fp;
-          o[j][2 + e] = o[j][2 + e] * f + part[(4 * j + 2 + e) * 32] * fp;
+      absorb([&](int i) { return part[i * 32]; });
+    }
+    if (a.team > 1) {      // (the barriers count the warps that have not returned)
+      if (rank > 0) publish();
+      cluster_barrier();
+      if (rank == 0)
+        for (int r = 1; r < a.team; ++r) {
+          const uint32_t part = cluster_address(own_smem, r) + lane * 4;
+          absorb([&](int i) { return load_cluster(part + i * 128); });
         }
-      }
+      cluster_barrier();      // what was read stays until then
+      if (rank > 0) return;
     }
   }
 #pragma unroll
@@ -1408,12 +1452,26 @@ cudaError_t launch_f32(const ChunkArgs& a, cudaStream_t st) {
 
 template <int D, bool E4M3, int NT, bool TEAM>
 cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t st) {
-  const dim3 grid(TEAM ? a.blocks : (a.blocks + kWarps - 1) / kWarps, a.Hkv * a.groups, a.L);
   const int smem = kWarps * warp_bytes<D, E4M3, NT, TEAM>(a.shift == 3);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
         k_chunk_tc<D, E4M3, NT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+  }
+  const dim3 grid(TEAM ? a.blocks * a.team : (a.blocks + kWarps - 1) / kWarps, a.Hkv * a.groups,
+                  a.L);
+  if (TEAM && a.team > 1) {
+    cudaLaunchAttribute cluster = {};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim = {(unsigned)a.team, 1, 1};
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(kWarps * 32);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    c.attrs = &cluster;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, k_chunk_tc<D, E4M3, NT, TEAM>, a);
   }
   k_chunk_tc<D, E4M3, NT, TEAM><<<grid, kWarps * 32, smem, st>>>(a);
   return cudaSuccess;
@@ -1421,7 +1479,7 @@ cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t st) {
 
 template <int D, bool E4M3, int NT>
 cudaError_t launch_nt(const ChunkArgs& a, cudaStream_t st) {
-  return a.team ? launch_tc<D, E4M3, NT, true>(a, st) : launch_tc<D, E4M3, NT, false>(a, st);
+  return a.team > 0 ? launch_tc<D, E4M3, NT, true>(a, st) : launch_tc<D, E4M3, NT, false>(a, st);
 }
 
 template <int D, bool E4M3>

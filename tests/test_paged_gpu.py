@@ -125,6 +125,54 @@ def test_chunk_matches_the_plain_form(case, prior):
     _check_chunk(t, q, out, lse, ref, dtype, min(W, max(t.held)) + S + 2 * len(offs))
 
 
+# (format, D, Hq, Hkv, W, S, offsets, old, new): few tokens with windows that the warps of one,
+# two, four and eight CTAs share, short sequences beside long ones
+LONG = [("plain", 64, 2, 2, 400, 4, FIB, [4200, 3], [1, 1]),
+        ("plain", 64, 2, 2, 700, 0, (3,), [4200, 650], [1, 2]),
+        ("e4m3", 64, 4, 2, 1500, 4, FIB, [4200, 0], [9, 3]),
+        ("plain", 128, 8, 1, 4000, 0, FIB, [4200], [1]), ("e4m3", 128, 8, 1, 4000, 4, FIB, [4200, 40], [1, 1]),
+        ("plain", 32, 1, 1, 4000, 16, (), [4200, 0], [5, 1]), ("e4m3", 16, 6, 2, 2500, 0, MANY, [4200], [2])]
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.3])
+@pytest.mark.parametrize("case", LONG, ids=[f"{c[0]}_{c[2]}x{c[1]}_w{c[4]}" for c in LONG])
+def test_long_windows_of_few_tokens(case, alpha):
+    """As the cases above; LSE has 2^-24 per member more, for the sum's additions."""
+    fmt, D, Hq, Hkv, W, S, offs, old, new = case
+    t = plain.Batch(1, Hkv, D, 64, old, new, BF, fmt, seed=D)
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn((1, t.N, Hq, D), generator=g).to(BF)
+    beta = torch.randn((1, t.N, Hq), generator=g)
+    out, lse = _run_chunk(t, q, [alpha], window=W, sinks=S, offsets=offs, beta=beta)
+    o, l, mag, big = plain.chunk(q.double(), t.keys, t.vals, t.cu, t.old, [alpha], W, S, offs,
+                                 beta=beta.double())
+    n = min(W, max(t.held)) + S + 2 * len(offs)
+    assert ((lse.double() - l).abs() <= 2.0 ** -20 * (big + l.abs() + 1) + 2.0 ** -24 * n).all()
+    tol = (2.0 ** -18 * (big[..., None] + 1) + 2.0 ** -24 * n + 2.0 ** -8) * mag
+    assert ((out.double() - o).abs() <= tol + 2.0 ** -8 * o.abs()).all()
+
+
+@pytest.mark.device_error_expected
+@pytest.mark.parametrize("fmt,D,W", [("plain", 64, 400), ("e4m3", 32, 1200), ("plain", 128, 4000)])
+def test_a_bad_page_anywhere_in_a_shared_window(fmt, D, W):
+    t = plain.Batch(1, 1, D, 64, [4200], [1], BF, fmt, seed=1)
+    cache, table, cu, cached = t.device(sa)
+    q = torch.randn((1, 1, 2, D), generator=torch.Generator().manual_seed(0)).to(BF).to(DEV)
+    alpha = torch.ones(1, device=DEV)
+    call = lambda: sa.chunk_attn(q, cache, table, cu, cached, alpha, window=W, offsets=(5,))
+    want = call()
+    assert sa.device_error(clear=True) == 0
+    for page in range(table.shape[1]):
+        good = table[0, page].clone()
+        table[0, page] = 1 << 20
+        o, lse = call()
+        table[0, page] = good
+        inside = (page + 1) * 64 > 4200 - W + 1 and page * 64 <= 4200
+        assert sa.device_error(clear=True) == (sa.ERR_PAGE if inside else 0), page
+        assert bool(torch.isnan(o).all()) == inside and bool(torch.isnan(lse).all()) == inside
+        assert inside or (torch.equal(o, want[0]) and torch.equal(lse, want[1]))
+
+
 @pytest.mark.parametrize("dtype,fmt,Hq,Hkv", [(BF, "plain", 1, 1), (BF, "e4m3", 4, 2),
                                               (F32, "plain", 2, 1), (F32, "e4m3", 1, 1)])
 def test_masked_rows_with_infinities_and_nan_do_not_reach_a_query(dtype, fmt, Hq, Hkv):
