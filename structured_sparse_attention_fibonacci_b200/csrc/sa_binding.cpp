@@ -220,12 +220,18 @@ sa_dtype row_type(ScalarType t) {
   return t == at::kFloat ? SA_DTYPE_F32 : SA_DTYPE_BF16;
 }
 
-// The library call without the interpreter's lock, and its status.
+// The library call without the interpreter's lock, and its status. (f may throw: a
+// tensor without storage has no address to give.)
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 template <typename F>
 void call(const char* name, F f) {
-  PyThreadState* s = PyEval_SaveThread();
-  const sa_status status = f();
-  PyEval_RestoreThread(s);
+  const sa_status status = [&] {
+    const Unlocked here;
+    return f();
+  }();
   if (status == SA_OK) return;
   PyObject* r = PyObject_CallFunction(g.check, "si", name, (int)status);
   Py_XDECREF(r);

@@ -714,3 +714,19 @@ def test_calls_by_keyword_and_with_other_numbers():
         sa.chunk_attn(cache=cache)
     with pytest.raises(TypeError):
         sa.chunk_attn()
+
+
+def test_tensors_without_storage_are_refused():
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    real = sa.paged_cache(1, 2, 1, 16, 32)
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        q = torch.empty((1, 2, 1, 5, 32), device=DEV)
+        with pytest.raises(Exception):
+            sa.qk_norm_rope(q, q, None, None)
+        x = torch.empty((1, 5, 1, 32), dtype=BF, device=DEV)
+        i32 = lambda *n: torch.empty(n, dtype=torch.int32, device=DEV)
+        with pytest.raises(Exception):
+            sa.cache_append(x, x, x, real, i32(1, 2), i32(2), i32(1))
+        with pytest.raises(Exception):
+            sa.chunk_attn(x, real, i32(1, 2), i32(2), i32(1), torch.ones(1, device=DEV), window=3)
+    assert sa.device_error() == 0
