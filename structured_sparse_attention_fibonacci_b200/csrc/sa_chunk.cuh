@@ -15,11 +15,10 @@
 // holds 8/G consecutive tokens. Scores are S^T = K q^T (M = 16 gathered rows,
 // N = 8 columns) and outputs O^T = V^T P^T (M = 16 head dims, N = 8 columns), so
 // that eight columns, not sixteen, have to be filled.
-//   - Gathered rows come in stages of 32 (36) by 16-byte asynchronous copies into
-//     the warp's own shared memory, two stages in flight, and become fragments
-//     by ldmatrix (transposed for V). Rows that go from global memory into
-//     registers directly took 241 us where this takes 219 (16384 tokens, 16 heads
-//     of 64, window 64, 4 sinks): they need the registers that hide the latency.
+//   - Gathered rows come in stages of 32 (36) by 16-byte asynchronous copies past the
+//     L1 into the warp's own shared memory, two stages in flight, and become fragments
+//     by ldmatrix (transposed for V). Rows that went from global memory into registers
+//     directly took 10 % more: they need the registers that hide the latency.
 //     Nothing waits but a warp for its own copies. tcgen05 has no form for the
 //     gather: its A operand is a tile of 128 rows, of which a token's 15
 //     interpolated pairs would fill a quarter.
@@ -35,9 +34,13 @@
 //   - Integer distances in the whole layer (KIND 1, 2): no row b. 16 offsets in a
 //     tile of one token, or 8 of two; an offset inside the window is a window row a
 //     second time and costs nothing but a larger score (189 -> 163 us at window 64).
-// Bound: at 16 warps an SM (128 registers) by latency and the L1 together: 2800
-// instructions and 900 wavefronts of the L1's data path per warp of 8 tokens at
-// window 64, 91 and 80 us of the 163.
+//   - Few blocks (one token each, a long window): the warps of up to eight CTAs share a
+//     block's window, one of them takes the offsets, and the parts (o, m, l) meet in
+//     shared memory, across CTAs through the cluster's.
+// Bound: issue, and the latency of dependent instructions that five warps a scheduler
+// leave: 2950 instructions per warp of 8 tokens at window 64, 57 % of the issue slots
+// (interpolated at window 12: 3200, 60 %; the L1's data path 51 and 72 %, the tensor
+// pipe 12 and 22 %).
 // Rounding: products of 16-bit values are exact, sums fp32. The probabilities are
 // rounded to bf16 for P V (2^-9 each on average, below the output's own rounding),
 // their sum is not. e4m3 codes are exact in fp16, and so are the queries beside
@@ -381,8 +384,8 @@ __device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, in
 
 // Bytes of a stage, and of a warp's shared memory: two stages, and (shared stages of
 // interpolated distances) a score per lane of each. Plain rows of 128 without shared
-// stages take 32 rows: the 8 KB per CTA are a fifth of what the L1 has left there
-// (16384 tokens, 32 heads over 4: 297 -> 274 us).
+// stages take 32 rows, which leaves the L1 24 KB more (16384 tokens, 32 heads over 4:
+// 251 -> 241 us).
 template <int D, bool E4M3>
 __host__ __device__ __forceinline__ constexpr int stage_bytes(bool shared) {
   return !E4M3 && D == 128 && !shared ? 32 * Stage<D, E4M3>::kRow : Stage<D, E4M3>::kBytes;
