@@ -241,14 +241,14 @@ def decode_bytes_per_token_head(wl, elt):
 # capture per entry; keyed by workload, kernel and the hash of the kernel
 # sources the capture ran (kernel_source_hash): a changed source reports null.
 MEASURED_TRAFFIC = {
-    "learned_train/bwd_q_fast@a3631b8328cf": 780.3,
-    "pi_gate_train/bwd_q_fast@a3631b8328cf": 545.8,
-    "paper_fwd/fwd_fast@a3631b8328cf": 494.4,
-    "extrap_4x/fwd_fast@a3631b8328cf": 496.1,
-    "pow2_extrap/fwd_fast@a3631b8328cf": 496.3,
-    "pi_skip/fwd_fast@a3631b8328cf": 492.1,
-    "long_sinks/fwd_tc@a3631b8328cf": 505.3,
-    "decode_4k/decode@a3631b8328cf": 8121.5,
+    "learned_train/bwd_q_fast@cfbf3273cb54": 778.8,
+    "pi_gate_train/bwd_q_fast@cfbf3273cb54": 545.3,
+    "paper_fwd/fwd_fast@cfbf3273cb54": 494.1,
+    "extrap_4x/fwd_fast@cfbf3273cb54": 495.8,
+    "pow2_extrap/fwd_fast@cfbf3273cb54": 496.0,
+    "pi_skip/fwd_fast@cfbf3273cb54": 491.1,
+    "long_sinks/fwd_tc@cfbf3273cb54": 508.4,
+    "decode_4k/decode@cfbf3273cb54": 8120.2,
 }
 
 
