@@ -387,8 +387,7 @@ def _chunk_plain(s):
     offs = pos[None, :, None] - d.ceil().long()[:, None, :] >= 0
     n_off = first.shape[-1]
     M = W + S + n_off
-    # (rows of no member are masked below; sinks may lie behind a short sequence's pages)
-    every = torch.cat([rows, first, second], -1).clamp(0, _rows(c) - 1)
+    every = torch.cat([rows, first, second], -1).clamp(min=0)
     page = s["table"].long()[b[None, :, None], every // c["page"]]
     l = torch.arange(L, device="cuda")[:, None, None, None]
     h = torch.arange(hkv, device="cuda")[None, None, :, None]
