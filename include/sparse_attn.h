@@ -387,8 +387,9 @@ sa_status sparse_attn_cache_read(const sa_paged_params* p, const sa_pages* pages
  *   lse   : device fp32 [L][N][Hq] or NULL                            (written)
  *   window, n_offsets, offsets (host), n_sinks, scale: as in sa_params; any
  *           window.
- * Scores and softmax are fp32; with bf16 queries the probabilities are rounded
- * to bf16 for their product with the values. Masked rows do not reach a query,
+ * Scores and softmax are fp32; with bf16 queries the probabilities enter their
+ * product with the values as sums of two bf16 numbers (e4m3 pages: times the row's
+ * scale, of two fp16 numbers): 16 bits or more. Masked rows do not reach a query,
  * whatever they hold. Source: the attended set, scaling and interpolation of
  * "Depth-Staggered Fibonacci Spacing for Sparse Attention" (Methodology).
  */

@@ -41,11 +41,15 @@
 // leave: 2950 instructions per warp of 8 tokens at window 64, 57 % of the issue slots
 // (interpolated at window 12: 3200, 60 %; the L1's data path 51 and 72 %, the tensor
 // pipe 12 and 22 %).
-// Rounding: products of 16-bit values are exact, sums fp32. The probabilities are
-// rounded to bf16 for P V (2^-9 each on average, below the output's own rounding),
-// their sum is not. e4m3 codes are exact in fp16, and so are the queries beside
-// them after scaling by a power of two; there probabilities times row scales are
-// rounded to fp16, relative to the largest of the column.
+// Rounding: products of 16-bit values are exact, sums fp32. The probabilities go into
+// P V as sums of two bf16 values, off by 2^-16 of themselves at most. One alone cost the
+// output a quarter more error than its own rounding (16384 tokens, 16 heads of 64,
+// window 64: 2.06e-3 of its 2-norm against 1.66e-3 with both, which is what fp32
+// probabilities give); the second product on the same fragments took 136 -> 145 us
+// there, and a mixed batch over e4m3 rows of 128 from 110 to 113. e4m3 codes are
+// exact in fp16, and so are the queries beside them after scaling by a power of two;
+// there probabilities times row scales are sums of two fp16 values (2^-22), relative
+// to the largest of the column.
 // A masked probability is 0, and 0 * Inf or NaN is NaN: a block with a non-finite
 // output is computed again query by query (one_query), from its members alone.
 //
@@ -123,6 +127,17 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
   } else {
     return pack_bf16x2(lo, hi);
+  }
+}
+// A pair as a sum of two 16-bit pairs: the rounded values and what that leaves, rounded.
+template <bool F16>
+__device__ __forceinline__ void split16(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack16<F16>(a, b);
+  if constexpr (F16) {
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    lo = pack16<true>(a - h.x, b - h.y);
+  } else {
+    lo = pack16<false>(a - bf16lo(hi), b - bf16hi(hi));
   }
 }
 
@@ -211,6 +226,11 @@ __device__ __forceinline__ float load_shared(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
   return x;
 }
+
+// P^T of a tile, rounded and what that leaves: p[0], p[1] for rows 0..7 and 8..15.
+struct Weights {
+  uint32_t hi[2], lo[2];
+};
 
 // A stage: 32 gathered rows (two tiles of 16) of K or V, in 16-byte chunks whose
 // place is exchanged by row (so that eight rows of one chunk column, an ldmatrix
@@ -338,18 +358,19 @@ struct Stage {
       }
     }
   }
-  // O^T += V^T P^T of a tile's 16 values; p0, p1: P^T for rows 0..7 and 8..15.
+  // O^T += V^T P^T of a tile's 16 values.
   // Lane g's head dims of product j: 16 j + g and 16 j + 8 + g, for e4m3 rows
   // 16 j + 2 g and the next.
   template <int OFFSET>
-  static __device__ __forceinline__ void add(uint32_t stage, uint32_t at, uint32_t p0, uint32_t p1,
+  static __device__ __forceinline__ void add(uint32_t stage, uint32_t at, const Weights& p,
                                              float (&o)[D / 16][4]) {
     if constexpr (!E4M3) {
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {
         uint32_t r[4];
         ldmatrix4<true, OFFSET>(stage + (at ^ (j << 5)), r);
-        mma16816<false>(o[j], r[0], r[1], r[2], r[3], p0, p1);
+        mma16816<false>(o[j], r[0], r[1], r[2], r[3], p.lo[0], p.lo[1]);
+        mma16816<false>(o[j], r[0], r[1], r[2], r[3], p.hi[0], p.hi[1]);
       }
     } else {
 #pragma unroll
@@ -362,19 +383,20 @@ struct Stage {
           uint32_t a0, a1, a2, a3;
           e4m3x4_to_f16x4(__byte_perm(r[j], 0, 0x3120), a0, a1);
           e4m3x4_to_f16x4(__byte_perm(r[2 + j], 0, 0x3120), a2, a3);
-          mma16816<true>(o[2 * i + j], a0, a1, a2, a3, p0, p1);
+          mma16816<true>(o[2 * i + j], a0, a1, a2, a3, p.lo[0], p.lo[1]);
+          mma16816<true>(o[2 * i + j], a0, a1, a2, a3, p.hi[0], p.hi[1]);
         }
       }
     }
   }
   // add() of tile `tile` (a constant after unrolling), STEP bytes from one to the next.
   template <int STEP>
-  static __device__ __forceinline__ void add_of(int tile, uint32_t stage, uint32_t at, uint32_t p0,
-                                                uint32_t p1, float (&o)[D / 16][4]) {
-    if (tile == 0) add<0>(stage, at, p0, p1, o);
-    if (tile == 1) add<STEP>(stage, at, p0, p1, o);
-    if (tile == 2) add<2 * STEP>(stage, at, p0, p1, o);
-    if (tile == 3) add<3 * STEP>(stage, at, p0, p1, o);
+  static __device__ __forceinline__ void add_of(int tile, uint32_t stage, uint32_t at,
+                                                const Weights& p, float (&o)[D / 16][4]) {
+    if (tile == 0) add<0>(stage, at, p, o);
+    if (tile == 1) add<STEP>(stage, at, p, o);
+    if (tile == 2) add<2 * STEP>(stage, at, p, o);
+    if (tile == 3) add<3 * STEP>(stage, at, p, o);
   }
 };
 
@@ -838,6 +860,13 @@ __global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3, TEAM>())
       }
     }
 
+    // P^T of half a tile from the lane's two columns of a row
+    auto transposed = [](Weights& p, int half, float a, float b) {
+      split16<E4M3>(a, b, p.hi[half], p.lo[half]);
+      p.hi[half] = transpose8(p.hi[half]);
+      p.lo[half] = transpose8(p.lo[half]);
+    };
+
     // ---- window and sinks, two tiles of 16 rows at a time ----
 #pragma unroll 1
     for (int t0 = t_first; t0 < t_past; t0 += t_step) {
@@ -920,8 +949,10 @@ __global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3, TEAM>())
           const float va = row_scale(stage, 1, i, 0), vc = row_scale(stage, 1, i, 1);
           p[0] *= va; p[1] *= va; p[2] *= vc; p[3] *= vc;
         }
-        Y::template add_of<Y::kTile>(i, stage, at_v, transpose8(pack16<E4M3>(p[0], p[1])),
-                                     transpose8(pack16<E4M3>(p[2], p[3])), o);
+        Weights pt;
+        transposed(pt, 0, p[0], p[1]);
+        transposed(pt, 1, p[2], p[3]);
+        Y::template add_of<Y::kTile>(i, stage, at_v, pt, o);
       }
       __syncwarp();
       if (more)
@@ -954,12 +985,16 @@ __global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3, TEAM>())
         const float a1 = __shfl_sync(0xffffffffu, pa, from + 4);
         const float b0 = __shfl_sync(0xffffffffu, pb, from);
         const float b1 = __shfl_sync(0xffffffffu, pb, from + 4);
-        const uint32_t fa = pack16<E4M3>(a0, a1), fb = pack16<E4M3>(b0, b1);
+        Weights f;
+        split16<E4M3>(a0, a1, f.hi[0], f.lo[0]);
+        split16<E4M3>(b0, b1, f.hi[1], f.lo[1]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (2 * j >= count) continue;      // uniform
           const bool on = g == 2 * j + (c >> 1);
-          Y::template add_of<2 * Y::kRow>(j, stage, at, on ? fa : 0u, on ? fb : 0u, o);
+          const Weights p = {{on ? f.hi[0] : 0u, on ? f.hi[1] : 0u},
+                             {on ? f.lo[0] : 0u, on ? f.lo[1] : 0u}};
+          Y::template add_of<2 * Y::kRow>(j, stage, at, p, o);
         }
         __syncwarp();
         if (st + 2 < n_off) rows_in(0, false);
@@ -971,7 +1006,7 @@ __global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3, TEAM>())
       const float z0 = m[0] == -INFINITY ? 0.f : m[0], z1 = m[1] == -INFINITY ? 0.f : m[1];
       // P^T of all columns (plain rows): lane (g, c) has column g, rows 2c and 2c + 1;
       // a token's product takes its own columns of it
-      [[maybe_unused]] uint32_t pa[NS], pb[NS];
+      [[maybe_unused]] Weights pt[NS];      // halves: rows a and b
       const int tok_g = token_of(g);
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
@@ -981,8 +1016,8 @@ __global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3, TEAM>())
         l[1] += sig[i][1];
         if constexpr (!E4M3) {
           const float wb = wg[i], wa = 1.f - wb;
-          pa[i] = transpose8(pack_bf16x2(sig[i][0] * wa, sig[i][1] * wa));
-          if (!FLAT) pb[i] = transpose8(pack_bf16x2(sig[i][0] * wb, sig[i][1] * wb));
+          transposed(pt[i], 0, sig[i][0] * wa, sig[i][1] * wa);
+          if (!FLAT) transposed(pt[i], 1, sig[i][0] * wb, sig[i][1] * wb);
         }
       }
       int k = 2;
@@ -1000,19 +1035,22 @@ __global__ void __launch_bounds__(kWarps * 32, chunk_ctas<D, E4M3, TEAM>())
             const int bt = KIND == 2 ? at + 1 : at;
             const int ia = KIND == 2 ? 0 : (FLAT ? 2 * pair : 2 * pair + i);
             const int ib = KIND == 1 ? 2 * pair + 1 : ia;
-            uint32_t p0, p1;
+            Weights p;
             if constexpr (E4M3) {
               const float wb = FLAT ? 1.f : wg[ia], wa = FLAT ? 1.f : 1.f - wb;
               const float va = row_scale(stage, 1, i, 0) * wa, vc = row_scale(stage, 1, i, 1) * wb;
-              p0 = transpose8(pack16<true>(tok[0] == at ? sig[ia][0] * va : 0.f,
-                                           tok[1] == at ? sig[ia][1] * va : 0.f));
-              p1 = transpose8(pack16<true>(tok[0] == bt ? sig[ib][0] * vc : 0.f,
-                                           tok[1] == bt ? sig[ib][1] * vc : 0.f));
+              transposed(p, 0, tok[0] == at ? sig[ia][0] * va : 0.f,
+                         tok[1] == at ? sig[ia][1] * va : 0.f);
+              transposed(p, 1, tok[0] == bt ? sig[ib][0] * vc : 0.f,
+                         tok[1] == bt ? sig[ib][1] * vc : 0.f);
             } else {
-              p0 = tok_g == at ? pa[ia] : 0u;
-              p1 = tok_g == bt ? (FLAT ? pa[ib] : pb[ib]) : 0u;
+              constexpr int hb = FLAT ? 0 : 1;
+              p.hi[0] = tok_g == at ? pt[ia].hi[0] : 0u;
+              p.lo[0] = tok_g == at ? pt[ia].lo[0] : 0u;
+              p.hi[1] = tok_g == bt ? pt[ib].hi[hb] : 0u;
+              p.lo[1] = tok_g == bt ? pt[ib].lo[hb] : 0u;
             }
-            Y::template add_of<Y::kTile>(i, stage, at_v, p0, p1, o);
+            Y::template add_of<Y::kTile>(i, stage, at_v, p, o);
           }
           __syncwarp();
           if (k < n_off) rows_in(pair, false);
