@@ -1494,9 +1494,13 @@ cudaError_t launch_f32(const ChunkArgs& a, cudaStream_t st) {
 template <int D, bool E4M3, int NT, bool TEAM>
 cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t st) {
   const int smem = kWarps * warp_bytes<D, E4M3, NT, TEAM>(a.shift == 3);
-  if (smem > 48 * 1024) {
+  // The limit is the process's: the instance's largest size whatever this call needs, so
+  // that calls of several threads do not lower it for each other.
+  constexpr int most = kWarps * warp_bytes<D, E4M3, NT, TEAM>(true);
+  static_assert(most >= kWarps * warp_bytes<D, E4M3, NT, TEAM>(false), "shared stages are larger");
+  if (most > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
-        k_chunk_tc<D, E4M3, NT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        k_chunk_tc<D, E4M3, NT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }
   const dim3 grid(TEAM ? a.blocks * a.team : (a.blocks + kWarps - 1) / kWarps, a.Hkv * a.groups,
