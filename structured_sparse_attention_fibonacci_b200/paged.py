@@ -75,12 +75,24 @@ def paged_cache(layers, n_pages, heads, page_size, head_dim, dtype=torch.bfloat1
                               for _ in range(2)))
 
 
-_native = None      # the extension module, once the library is loaded
+_native = None      # the extension module, once one of its calls was made
 
 
 def _calls():
+    """The extension module, given the library's entry points."""
+    global _native
     if _native is None:
-        lib()
+        L = lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"{__package__}._binding cannot be loaded ({e}): build it with "
+                               f"`python -m {__package__}.build`") from e
+        _binding.bind(_check, *[ctypes.cast(getattr(L, "sparse_attn_" + n), ctypes.c_void_p).value
+                                for n in ("qk_norm_workspace_size", "qk_norm_rope",
+                                          "qk_norm_rope_bwd", "cache_append", "cache_read",
+                                          "chunk")])
+        _native = _binding
     return _native
 
 
@@ -165,9 +177,7 @@ def chunk_attn(q, cache, page_table, cu_q, cached, alpha, *, window, offsets=FIB
 
 
 def _bind(L):
-    """Argument types of the entry points (structures are passed by reference), and
-    their addresses for the extension module."""
-    global _native
+    """Argument types of the entry points (structures are passed by reference)."""
     vp, sz, i32, f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_float
     NP, HS = ctypes.POINTER(QkNormParams), ctypes.POINTER(HeadStrides)
     PP, PG, RS = ctypes.POINTER(PagedParams), ctypes.POINTER(Pages), ctypes.POINTER(RowStrides)
@@ -182,12 +192,3 @@ def _bind(L):
             ("chunk", [PP, PG, vp, vp, vp, RS, vp, vp, i32, i32, vp, i32, f32, vp, vp, vp])):
         f = getattr(L, "sparse_attn_" + name)
         f.restype, f.argtypes = ctypes.c_int, args
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise RuntimeError(f"{__package__}._binding is missing: build it with "
-                           f"`python -m {__package__}.build`") from e
-    _binding.bind(_check, *[ctypes.cast(getattr(L, "sparse_attn_" + n), vp).value for n in (
-        "qk_norm_workspace_size", "qk_norm_rope", "qk_norm_rope_bwd", "cache_append", "cache_read",
-        "chunk")])
-    _native = _binding
