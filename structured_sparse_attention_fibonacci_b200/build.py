@@ -14,7 +14,10 @@ binding loads with ctypes:
                             the parity tests can run under it in place of a
                             memory checker;
 and csrc/sa_binding.cpp with nvcc's host compiler, against the installed torch:
-  _binding.so               extension module behind paged.py's calls.
+  _binding.so               extension module behind paged.py's calls;
+  _binding.built_for        the torch and the Python that it was built for: another
+                            one's classes and interface may differ, so it is built
+                            again for them.
 """
 import concurrent.futures as cf
 import glob
@@ -30,6 +33,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsparse_attn.so")
 LIB_BOUNDS = os.path.join(HERE, "libsparse_attn_bounds.so")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_FOR = os.path.join(HERE, "_binding.built_for")
 BINDING_SRC = os.path.join(CSRC, "sa_binding.cpp")
 OBJ_DIR = os.path.join(HERE, "_build")
 
@@ -47,11 +51,23 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _built_for():
+    """The installed torch and Python, as far as compiled code depends on them."""
+    import torch
+    return (f"torch {torch.__version__} cxx11_abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} "
+            f"{sysconfig.get_config_var('SOABI')}\n")
+
+
 def _stale(lib):
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
     if lib == BINDING:
+        if not os.path.exists(BINDING_FOR):
+            return True
+        with open(BINDING_FOR) as f:
+            if f.read() != _built_for():
+                return True
         deps = (BINDING_SRC, os.path.join(INCLUDE, "sparse_attn.h"), os.path.abspath(__file__))
         return any(os.path.getmtime(d) > t for d in deps)
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
@@ -82,7 +98,12 @@ def _build_binding(nvcc, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
+    if os.path.exists(BINDING_FOR):
+        os.remove(BINDING_FOR)      # an interrupted build leaves a stale one
     os.replace(tmp, BINDING)
+    with open(tmp, "w") as f:
+        f.write(_built_for())
+    os.replace(tmp, BINDING_FOR)
 
 
 def build(force: bool = False, verbose: bool = False, extra=(), variants=None) -> str:

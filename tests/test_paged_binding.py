@@ -39,3 +39,22 @@ for _ in range(2):
         raise AssertionError("no error")
 """)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("change", ["torch", "missing", "module", "nothing"])
+def test_the_extension_module_is_built_again_for_another_torch(change, tmp_path, monkeypatch):
+    """Stale for another torch or Python than it was built for, whatever its file's time; only
+    then is it built."""
+    for name in ("BINDING", "BINDING_FOR"):
+        path = tmp_path / name
+        path.write_text(sa_build._built_for())
+        monkeypatch.setattr(sa_build, name, str(path))
+    if change == "torch":
+        (tmp_path / "BINDING_FOR").write_text("torch 0.0\n")
+    elif change != "nothing":
+        (tmp_path / {"missing": "BINDING_FOR", "module": "BINDING"}[change]).unlink()
+    assert sa_build._stale(sa_build.BINDING) == (change != "nothing")
+    built = []
+    monkeypatch.setattr(sa_build, "_build_binding", lambda *a: built.append(1))
+    sa_build.build()
+    assert len(built) == (change != "nothing")
