@@ -258,6 +258,8 @@ sa_status sparse_attn_decode_prior(const sa_params* p, int32_t pos, const void* 
  *   workspace : at least sparse_attn_qk_norm_workspace_size bytes, 16-byte
  *       aligned; one call's at a time (calls that may overlap, captured graphs
  *       among them, need one each). 0 bytes without weights.
+ * Apart from what is said of q_out, k_out, dq and dk, no array that is written shares
+ * memory with another one of the call.
  * B = 0 or T = 0 is a call without rows: it writes zero weight gradients.
  * The first call with a head dim, a rope_base and more positions than before makes
  * a table of cosines on the device (kept, as the forward's) and waits for it: under
@@ -320,6 +322,9 @@ sa_status sparse_attn_qk_norm_rope_bwd(const sa_qk_norm_params* p, const void* q
  * neighbouring tokens of the sequence. No two sequences with new tokens may write
  * to the same page.
  *
+ * No array that a call writes (the pages of an append among them) shares memory with
+ * another one of the call.
+ *
  * Limits: D in {16, 32, 64, 128}; max_pages * page_size <= 2^24; n_pages * Hkv *
  * page_size < 2^31; L and Hq + 2 Hkv at most 65535 (cache_read: B * Hkv). N = 0
  * and B = 0 are calls without work.
@@ -352,7 +357,7 @@ typedef struct {
  * 16-byte aligned, both or neither) queries and keys are normed first, as in
  * sparse_attn_qk_norm_rope. q, k, v: rows [L][N][heads][D] of any strides that
  * are multiples of 16 bytes (slices of one projection's output), 16-byte aligned;
- * q_out: contiguous [L][N][Hq][D], not overlapping them. The table of cosines is as
+ * q_out: contiguous [L][N][Hq][D]. The table of cosines is as
  * long as the page table reaches, so one call before a capture suffices.
  */
 sa_status sparse_attn_cache_append(const sa_paged_params* p, const sa_pages* pages,

@@ -290,8 +290,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t count) {
   const Place at(q, stream);
   const Norm n = norm_args(a, q, at);
   const Tensor *q_out = a.optional("q_out"), *k_out = a.optional("k_out");
-  const Tensor qo = output("q_out", q_out, q, at, {&n.k, k_out});
-  const Tensor ko = output("k_out", k_out, n.k, at, {&q});
+  const Tensor qo = output("q_out", q_out, q, at, {&n.k, n.qw, n.kw, k_out});
+  const Tensor ko = output("k_out", k_out, n.k, at, {&q, n.qw, n.kw});
   call("sparse_attn_qk_norm_rope", [&] {
     return g.norm(&n.p, in(&q), &n.qs, in(&n.k), &n.ks, in<float>(n.qw), in<float>(n.kw),
                   out_of(qo), out_of(ko), at.stream());
@@ -313,17 +313,19 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* args, Py_ssize_t count) {
   const Tensor* given = a.optional("workspace");
   const sa_head_strides dqs = head_rows("dq_out", dq_out, q.sizes(), q.scalar_type(), at);
   const sa_head_strides dks = head_rows("dk_out", dk_out, n.k.sizes(), q.scalar_type(), at);
-  const Tensor dq = output("dq", dq_, dq_out, at, {&q, &n.k, &dk_out, dk_});
-  const Tensor dk = output("dk", dk_, dk_out, at, {&q, &n.k, &dq_out});
+  const Tensor dq = output("dq", dq_, dq_out, at, {&q, &n.k, &dk_out, n.qw, n.kw, dk_});
+  const Tensor dk = output("dk", dk_, dk_out, at, {&q, &n.k, &dq_out, n.qw, n.kw});
   Tensor dqw, dkw, ws;
   if (n.qw) {
-    dqw = output("dq_weight", dqw_, *n.qw, at, {dkw_});
-    dkw = output("dk_weight", dkw_, *n.kw, at, {&dqw});
+    dqw = output("dq_weight", dqw_, *n.qw, at, {&q, &n.k, &dq_out, &dk_out, &dq, &dk, dkw_});
+    dkw = output("dk_weight", dkw_, *n.kw, at, {&q, &n.k, &dq_out, &dk_out, &dq, &dk});
     if (!given) {
       ws = at::empty({(int64_t)g.workspace_size(&n.p)}, q.options().dtype(at::kByte));
     } else {
       if (!given->is_cuda() || given->get_device() != at.index || !given->is_contiguous())
         refuse("workspace must be a contiguous buffer on cuda:" + std::to_string(at.index));
+      apart("workspace", *given, nullptr,
+            {&q, &n.k, &dq_out, &dk_out, n.qw, n.kw, &dq, &dk, &dqw, &dkw});
       ws = *given;
     }
   } else if (dqw_ || dkw_) {
@@ -351,6 +353,11 @@ struct Cache {
     const Tensor &k = a.tensor("cache.k"), &v = a.tensor("cache.v");
     const Tensor* ks = a.optional("cache.k_scale");
     return {k, v, ks, a.optional("cache.v_scale")};
+  }
+  // Refuses a tensor that shares memory with the pages or their scales.
+  void apart_from(const char* name, const Tensor& t) const {
+    for (const Tensor* x : {&k, &v, k_scale, v_scale})
+      if (x && overlap(t, *x)) refuse(std::string(name) + " overlaps the cache");
   }
 };
 struct Paged {
@@ -424,9 +431,16 @@ PyObject* cache_append(PyObject*, PyObject* const* args, Py_ssize_t count) {
     out = empty(q);
   } else {
     whole("q_out", *given, q.sizes(), type, at);
-    apart("q_out", *given, nullptr, {&q, &k, &v});
+    apart("q_out", *given, nullptr, {&q, &k, &v, qw, kw, &table, &cu, &cached});
+    cache.apart_from("q_out", *given);
     out = *given;
   }
+  // (the pages are written: nothing else of the call may lie in them)
+  apart("cache.k", cache.k, nullptr, {&cache.v, cache.k_scale, cache.v_scale});
+  apart("cache.v", cache.v, nullptr, {cache.k_scale, cache.v_scale});
+  if (cache.k_scale) apart("cache.k_scale", *cache.k_scale, nullptr, {cache.v_scale});
+  for (const Tensor* t : {&q, &k, &v, qw, kw, &table, &cu, &cached})
+    if (t) cache.apart_from("an input", *t);
   call("sparse_attn_cache_append", [&] {
     return g.append(&x.p, &x.c, in<int32_t>(&cu), in<int32_t>(&cached), in(&q), &qs, in(&k), &ks,
                     in(&v), &vs, in<float>(qw), in<float>(kw), eps, base, out_of(out),
@@ -467,6 +481,10 @@ PyObject* cache_read(PyObject*, PyObject* const* args, Py_ssize_t count) {
     whole("k_out", *k_out, shape, type, at);
     whole("v_out", *v_out, shape, type, at);
     apart("v_out", *v_out, nullptr, {k_out});
+    for (const Tensor* t : {k_out, v_out}) {
+      cache.apart_from(t == k_out ? "k_out" : "v_out", *t);
+      apart(t == k_out ? "k_out" : "v_out", *t, nullptr, {&table, &lengths});
+    }
     k = *k_out;
     v = *v_out;
   } else {
@@ -519,11 +537,14 @@ PyObject* chunk_attn(PyObject*, PyObject* const* args, Py_ssize_t count) {
     out = empty(q);
   } else {
     whole("out", *out_, q.sizes(), type, at);
-    apart("out", *out_, nullptr, {&q});
+    apart("out", *out_, nullptr, {&q, &table, &cu, &cached, &alpha, beta, lse_});
+    cache.apart_from("out", *out_);
     out = *out_;
   }
   if (lse_) {
     whole("lse", *lse_, {L, N, Hq}, at::kFloat, at);
+    apart("lse", *lse_, nullptr, {&q, &table, &cu, &cached, &alpha, beta});
+    cache.apart_from("lse", *lse_);
     lse = *lse_;
   } else if (want_lse) {
     lse = at::empty({L, N, Hq}, alpha.options());

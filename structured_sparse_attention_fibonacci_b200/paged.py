@@ -16,7 +16,9 @@ types and devices of the tensors in ``csrc/sa_binding.cpp``, values in the libra
 
 All tensors of a call are on one CUDA device, which need not be the current
 one; the work goes to that device's current stream, or to ``stream=`` (every
-call takes it).
+call takes it). Outputs, the pages of an append and workspaces share no memory with
+the call's other tensors, but where a call says that an output may be an input;
+others are refused.
 """
 import ctypes
 from typing import NamedTuple, Optional
