@@ -461,19 +461,19 @@ PyObject* cache_read(PyObject*, PyObject* const* args, Py_ssize_t count) {
   const Tensor *k_out = a.optional("k_out"), *v_out = a.optional("v_out");
   both("k_out and v_out", k_out, v_out);
   ScalarType type = cache.k.scalar_type();
-  if (k_out) {
-    type = k_out->scalar_type();
-  } else if (kind != Py_None) {
+  if (kind != Py_None) {
     if (!THPDtype_Check(kind)) refuse_type("dtype must be a torch.dtype");
     type = reinterpret_cast<THPDtype*>(kind)->scalar_type;
+  } else if (k_out) {
+    type = k_out->scalar_type();
   } else if (type == at::kFloat8_e4m3fn) {
     type = at::kBFloat16;
   }
   const Paged x = paged_args(cache, table, type, -1, 0, -1, at);
   whole("lengths", lengths, {x.p.B}, at::kInt, at);
-  const int64_t rows = k_out             ? (k_out->dim() == 5 ? k_out->size(3) : -1)
-                       : asked != Py_None ? Args::int32(asked)
-                                          : (int64_t)x.p.max_pages * x.p.page_size;
+  const int64_t rows = asked != Py_None ? Args::int32(asked)
+                       : k_out          ? (k_out->dim() == 5 ? k_out->size(3) : -1)
+                                        : (int64_t)x.p.max_pages * x.p.page_size;
   if (rows < 0) refuse("k_out and v_out must be [L, B, Hkv, rows, D], rows at least 0");
   const int64_t shape[5] = {x.p.L, x.p.B, x.p.Hkv, rows, x.p.D};
   Tensor k, v;

@@ -157,8 +157,8 @@ def cache_read(cache, page_table, lengths, *, rows=None, dtype=None, k_out=None,
     """The first lengths[b] rows of every sequence (int32 [B]) as contiguous
     (k, v) [L, B, Hkv, rows, D] (sparse_attn_cache_read): the stored, rotated keys
     and the values; float8_e4m3fn pages are read as dtype (bf16 by default).
-    rows defaults to all that the page table covers, or to k_out's; rows from
-    lengths[b] on are left as they were (zeros where the output is made here)."""
+    rows defaults to all that the page table covers, or to k_out's (whose rows and
+    dtype any given rows= and dtype= have to be); rows from lengths[b] on are left as they were (zeros where the output is made here)."""
     return _calls().cache_read(stream, cache, page_table, lengths, rows, dtype, k_out, v_out)
 
 

@@ -150,3 +150,18 @@ def test_outputs_inside_other_tensors_of_a_norm_call_are_refused():
     d1, d2 = dyq.clone(), dyk.clone()
     for a, b in zip(bwd(), sa.qk_norm_rope_bwd(q, k, qw, kw, d1, d2, dq=d1, dk=d2)):
         assert torch.equal(a, b)
+
+
+def test_read_outputs_are_what_the_call_asks_for():
+    """rows= and dtype= beside outputs that have others: refused, not passed over."""
+    cache = sa.paged_cache(L, P, HKV, PAGE, D, Q8)
+    table, lengths = i32([[0, 1], [2, 3]]), i32([9, 3])
+    k, v = (torch.zeros((L, B, HKV, 8, D), dtype=BF, device=DEV) for _ in range(2))
+    for kw in (dict(rows=5), dict(rows=9), dict(rows=0), dict(dtype=F32), dict(rows=8, dtype=F32)):
+        with pytest.raises(ValueError):
+            sa.cache_read(cache, table, lengths, k_out=k, v_out=v, **kw)
+    for kw in (dict(), dict(rows=8), dict(dtype=BF), dict(rows=8, dtype=BF)):
+        got = sa.cache_read(cache, table, lengths, k_out=k, v_out=v, **kw)
+        assert got[0].data_ptr() == k.data_ptr() and got[1].data_ptr() == v.data_ptr()
+    with pytest.raises(TypeError):
+        sa.cache_read(cache, table, lengths, k_out=k, v_out=v, dtype="bf16")
