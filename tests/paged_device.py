@@ -158,3 +158,16 @@ def beyond(t, out, lse, ref):
         tol = tol + 2.0 ** -24 * o.abs()
     bad = ((out.double() - o).abs() - tol).amax().item()
     return bad, ((lse.double() - l).abs() - 2.0 ** -20 * (big + l.abs() + 1) - 2.0 ** -24 * M).amax().item()
+
+
+def rope(x, pos, base=10000.0, sign=1.0):
+    """x [..., D] in 64 bits, rotated at positions pos (broadcast against x's leading shape)."""
+    D = x.shape[-1]
+    theta = base ** (-2.0 * torch.arange(D // 2, dtype=torch.float64, device=DEV) / D)
+    a = sign * pos.double()[..., None] * theta
+    x1, x2 = x[..., :D // 2], x[..., D // 2:]
+    return torch.cat([x1 * a.cos() - x2 * a.sin(), x2 * a.cos() + x1 * a.sin()], -1)
+
+
+def norm(x, w, eps):
+    return x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps) * w
