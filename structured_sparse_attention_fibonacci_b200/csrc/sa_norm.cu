@@ -305,6 +305,9 @@ __global__ void __launch_bounds__(kDwThreads) k_qk_norm_dw(const float* part, in
 // of 64: 164 us with one wave, 141 with two, 130 with four), short ones pay for
 // each CTA's start and partial sums (2 x 3 x (12 + 4) x 777 rows of 128: 18, 21, 26;
 // all before the early launch of the second kernel, which takes 1 to 2 us off).
+// Beyond that as many as leave a CTA about 64 items: a thread adds a row of each to its
+// fp32 sums of dw, whose error would else grow with the batch (it is at most (rows +
+// 24) 2^-24 of the terms' sizes; the partial sums are added in 64 bits).
 struct BwdGrid {
   int n_q, blocks;
 };
@@ -313,7 +316,8 @@ BwdGrid bwd_grid(const NormProblem& p) {
   const long long tiles = ((long long)p.B * p.T + per - 1) / per;
   const long long waves =
       std::min(4LL, std::max(1LL, tiles * (p.Hq + p.Hkv) * p.L / (296 * 16)));
-  const long long want = std::max(2LL, (296 * waves + p.L - 1) / p.L);
+  const long long want = std::max({2LL, (296 * waves + p.L - 1) / p.L,
+                                   (tiles * (p.Hq + p.Hkv) + 63) / 64});
   const long long q = std::max(1LL, std::min(tiles * p.Hq, want * p.Hq / (p.Hq + p.Hkv)));
   const long long k = std::max(1LL, std::min(tiles * p.Hkv, want - want * p.Hq / (p.Hq + p.Hkv)));
   return {(int)q, (int)(q + k)};

@@ -155,3 +155,20 @@ def test_appends_of_several_passes(case, normed):
         if y is not None:
             y, z = (a.view(torch.uint8).view(*cache.k.shape[:4], -1).transpose(2, 3)[:, ~touched] for a in (y, z))
             assert torch.equal(y, z)
+
+
+def test_weight_gradients_of_a_long_batch_keep_their_bits():
+    """9 million rows that are all the same, so that every rounding of a running fp32 sum falls the
+    same way: n equal terms are off by up to n / 2 2^-24 of their sum. A thread may add 66 rows before
+    the sums go on in 64 bits: 33, and 16 for the warp's, the CTA's and each term's own roundings."""
+    T, Hq, Hkv, D = 2_280_011, 4, 1, 128
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x, dy = (torch.randn(D, generator=g, device=DEV).to(BF) for _ in range(2))
+    all_ = lambda r, h: r.expand(1, 1, h, T, D)
+    w = torch.ones((1, D), device=DEV)
+    _, _, dqw, dkw = sa.qk_norm_rope_bwd(all_(x, Hq), all_(x, Hkv), w, w, all_(dy, Hq), all_(dy, Hkv),
+                                         eps=0.0, rotate=False)
+    term = dy.double() * x.double() / torch.sqrt(x.double().square().mean())
+    for got, h in ((dqw, Hq), (dkw, Hkv)):
+        want = term * (T * h)
+        assert ((got[0].double() - want).abs() <= 49 * 2.0 ** -24 * want.abs()).all()
