@@ -357,8 +357,10 @@ typedef struct {
  * 16-byte aligned, both or neither) queries and keys are normed first, as in
  * sparse_attn_qk_norm_rope. q, k, v: rows [L][N][heads][D] of any strides that
  * are multiples of 16 bytes (slices of one projection's output), 16-byte aligned;
- * q_out: contiguous [L][N][Hq][D]. The table of cosines is as
- * long as the page table reaches, so one call before a capture suffices.
+ * q_out: contiguous [L][N][Hq][D]. The table of cosines is as long as the page table
+ * reaches (max_pages * page_size positions rounded up to a power of two, 4 D bytes
+ * each, kept until the process ends: 512 MB for 2^20 positions at D = 128), so one
+ * call before a capture suffices; size max_pages to the positions that are served.
  */
 sa_status sparse_attn_cache_append(const sa_paged_params* p, const sa_pages* pages,
                                    const int32_t* cu_q, const int32_t* cached, const void* q,
@@ -371,8 +373,8 @@ sa_status sparse_attn_cache_append(const sa_paged_params* p, const sa_pages* pag
 /*
  * Read back: rows 0 .. lengths[b] - 1 (lengths: device int32 [B]) of every
  * sequence to contiguous k and v [L][B][Hkv][rows][D] of params.dtype; at most
- * `rows` of them, and rows from lengths[b] on stay as they were. N and Hq are not
- * looked at.
+ * `rows` of them, and rows from lengths[b] on stay as they were. N and Hq have to be
+ * valid (0 and Hkv, say) and are not used.
  */
 sa_status sparse_attn_cache_read(const sa_paged_params* p, const sa_pages* pages,
                                  const int32_t* lengths, int32_t rows, void* k, void* v,
@@ -452,8 +454,8 @@ sa_status sparse_attn_fwd_noalloc(const sa_params* p, const void* q, const void*
                                   void* stream);
 
 /*
- * Device error word of the staged and the paged kernels.  Reading synchronises with the
- * device; with clear != 0 the word is reset.  Returns -1 on a CUDA error.
+ * Device error word of the staged and the paged kernels, of the current device.
+ * Reading synchronises with the device; with clear != 0 the word is reset.  Returns -1 on a CUDA error.
  *   bit 0: a bounded wait for a staging copy gave up (the kernel then left
  *          its outputs incomplete and returned rather than wait without end);
  *   bit 1: a row index outside the rows staged in shared memory, or a staging

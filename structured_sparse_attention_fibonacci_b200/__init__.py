@@ -12,7 +12,8 @@ present, the calls raise.
 
 ``paged.py`` binds the query/key norm, the paged cache and the attention over
 it (qk_norm_rope, cache_append, cache_read, chunk_attn) through an extension
-module, since their smallest calls are shorter than ctypes takes.
+module, loaded with the first of them, since their smallest calls are shorter than
+ctypes takes.
 
 Method: "Depth-Staggered Fibonacci Spacing for Sparse Attention" (C. A.
 Capps), technical summary, Methodology -- "Attended set", "Scaling",
@@ -186,7 +187,7 @@ def select_forward(which: int = 0) -> None:
 
 
 def device_error(clear: bool = True) -> int:
-    """Device error word of the staged kernels (ERR_WAIT: a bounded staging
+    """Device error word of the kernels on the current device (ERR_WAIT: a bounded staging
     wait gave up; ERR_BOUNDS: a bounds violation seen by the bounds-checking
     build; ERR_RANGE: an input beyond the staged operands' fp16 range; ERR_PAGE:
     a page index or a position of the paged cache outside its range);

@@ -32,11 +32,16 @@ cudaError_t launch_chunk_attn(const PagedProblem& p, const PagedPtrs& c, const C
                          (1 << a.shift) - 1;
   // Few blocks, as in a decode step, and a window of three tiles or more (the sinks
   // are one): a CTA's warps share a block while all CTAs are resident at once, four
-  // per SM, of plain rows of 128 three (one token, 16 heads, window 64 with sinks:
-  // 8.9 -> 6.9 us; with a window of one pair of tiles the join costs what it saves).
+  // per SM, of plain rows of 128 three. One token each of 8 sequences of 16 heads of 64
+  // with 4 sinks (128 blocks): 8.4 -> 6.4 us at window 64, 14.5 -> 8.3 at 256, 38 -> 12
+  // at 1024; of 32 sequences (512 blocks) 8.9 -> 7.2, 14.8 -> 9.6, 42 -> 26. Past the
+  // limit (640 blocks) a block per warp: 9.3 us where sharing takes 11.2 at window 64,
+  // 16.2 against 16.4 at 256, 45 against 44 at 1024. (Blocks are estimated here, up to
+  // an eighth too many. With a window of one pair of tiles the join costs what it
+  // saves.)
   // Clusters of two, four or eight CTAs share it where each of their warps has more
-  // than four pairs left (window 1024: 14.2 us by one CTA, 8.9 by two; 4096: 40 by one,
-  // 12.7 by eight).
+  // than four pairs left (one token, 16 heads, window 512: 10.8 us by one CTA, 8.7 by
+  // two; 1024: 15.4 and 9.2; 4096: 46 by one, 13.1 by eight).
   const bool f32 = p.dtype == SA_DTYPE_F32, q8 = p.format == SA_CACHE_E4M3;
   const long long tiles = (rows + 15) / 16 + (x.S > 0), pairs = (tiles + 1) / 2;
   const long long room = 148 * (p.D == 128 && !q8 ? 3 : 4);

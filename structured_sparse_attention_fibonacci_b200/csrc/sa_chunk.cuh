@@ -30,22 +30,24 @@
 //     of such a tile count; over the block's tokens a lane keeps its own.
 //   - One query head per key head (KIND 3): 8 tokens in a row read 9 rows of an
 //     offset, not 16, so a stage holds 4 offsets x 9 rows and serves 4 tiles of two
-//     tokens each (228 -> 197 us at window 12).
+//     tokens each (16384 tokens, 16 heads of 64, window 12: 182 -> 170 us).
 //   - Integer distances in the whole layer (KIND 1, 2): no row b. 16 offsets in a
 //     tile of one token, or 8 of two; an offset inside the window is a window row a
-//     second time and costs nothing but a larger score (189 -> 163 us at window 64).
+//     second time and costs nothing but a larger score (16384 tokens behind 16384, 16
+//     heads of 64: 164 -> 144 us at window 64; at 1024 the look at each score costs
+//     more than the few tiles, 713 -> 770).
 //   - Few blocks (one token each, a long window): the warps of up to eight CTAs share a
 //     block's window, one of them takes the offsets, and the parts (o, m, l) meet in
 //     shared memory, across CTAs through the cluster's.
 // Bound: issue, and the latency of dependent instructions that five warps a scheduler
-// leave: 2950 instructions per warp of 8 tokens at window 64, 57 % of the issue slots
-// (interpolated at window 12: 3200, 60 %; the L1's data path 51 and 72 %, the tensor
-// pipe 12 and 22 %).
+// leave: 3110 instructions per warp of 8 tokens at window 64, 56 % of the issue slots
+// (interpolated at window 12: 3380, 59 %; the L1's data path 46 and 64 %, the tensor
+// pipe 16 and 29 %).
 // Rounding: products of 16-bit values are exact, sums fp32. The probabilities go into
 // P V as sums of two bf16 values, off by 2^-16 of themselves at most. One alone cost the
 // output a quarter more error than its own rounding (16384 tokens, 16 heads of 64,
 // window 64: 2.06e-3 of its 2-norm against 1.66e-3 with both, which is what fp32
-// probabilities give); the second product on the same fragments took 136 -> 145 us
+// probabilities give); the second product on the same fragments took 136 -> 144 us
 // there, and a mixed batch over e4m3 rows of 128 from 110 to 113. e4m3 codes are
 // exact in fp16, and so are the queries beside them after scaling by a power of two;
 // there probabilities times row scales are sums of two fp16 values (2^-22), relative
@@ -56,7 +58,9 @@
 // 32-bit queries (k_chunk_f32, one_query): one warp per token and up to 4 query heads of
 // a key/value head on the CUDA cores, chunks of 32 members: four lanes per member for
 // the scores, lanes over head dims for the values. 4096 tokens, 16 heads of 64, window
-// 12: 181 us; two groups of 8 of them: 176 us head by head, 91 in fours.
+// 12: 180 us; two groups of 8 of them: 176 us head by head, 91 in fours. Bound: the L1,
+// whose data path is busy 76 % of the time (1800 instructions per token and head, 56 %
+// of the issue slots): tokens share no rows, so each loads its 42 again.
 #pragma once
 
 #include <type_traits>
@@ -174,8 +178,8 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t& lo, uin
 }
 
 // Past the L1: its data path is half of what the kernel waits for, and a row that passes
-// through it crosses it twice (16384 tokens, 16 heads of 64: window 64 162 -> 142 us,
-// interpolated, window 12 196 -> 168; 8 heads of 128: 203 -> 159).
+// through it crosses it twice (16384 tokens, 16 heads of 64: window 64 162 -> 144 us,
+// interpolated, window 12 198 -> 170; 8 heads of 128: 198 -> 160).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -407,7 +411,7 @@ __device__ __noinline__ void one_query(const ChunkArgs& a, int layer, int hq, in
 // Bytes of a stage, and of a warp's shared memory: two stages, and (shared stages of
 // interpolated distances) a score per lane of each. Plain rows of 128 without shared
 // stages take 32 rows, which leaves the L1 24 KB more (16384 tokens, 32 heads over 4:
-// 251 -> 241 us).
+// 262 -> 249 us).
 template <int D, bool E4M3>
 __host__ __device__ __forceinline__ constexpr int stage_bytes(bool shared) {
   return !E4M3 && D == 128 && !shared ? 32 * Stage<D, E4M3>::kRow : Stage<D, E4M3>::kBytes;
@@ -428,10 +432,11 @@ struct Walk {
 // a.team CTAs share one block (an instance of its own: the shares cost the others 4 %).
 // CTAs per SM, and with them the registers (96 a thread for five): more warps hide more
 // of the latency until the spills cost as much. 16384 tokens, plain rows: 16 heads of 64,
-// window 64 142 us with four, 136 with five; 32 heads of 128 over 4 258 with four, 241
-// with three; 16 heads of 16 102 with six, 117 with eight. e4m3 rows of 128: 219 with
-// four, 247 with three. Of teams there are at most four per SM (one token, 16 heads of
-// 64, window 4096 by one CTA: 49 us with registers for five, 40 for four).
+// window 64 149 us with four, 144 with five, 178 with six; 32 heads of 128 over 4 261
+// with four, 249 with three; 16 heads of 16 112 with five, 108 with six, 121 with eight.
+// e4m3 rows of 128: 253 with three, 224 with four, 284 with five. Of teams there are at
+// most four per SM (one token, 16 heads of 64, window 4096 by one CTA: 55 us with
+// registers for five, 46 for four).
 template <int D, bool E4M3, bool TEAM>
 __host__ __device__ __forceinline__ constexpr int chunk_ctas() {
   return D == 128 ? (E4M3 ? 4 : 3) : TEAM ? 4 : D == 64 ? 5 : 6;

@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(kDwThreads) k_qk_norm_dw(const float* part, in
 // all before the early launch of the second kernel, which takes 1 to 2 us off).
 // Beyond that as many as leave a CTA about 64 items: a thread adds a row of each to its
 // fp32 sums of dw, whose error would else grow with the batch (it is at most (rows +
-// 24) 2^-24 of the terms' sizes; the partial sums are added in 64 bits).
+// 24) 2^-24 of the terms' sizes; the partial sums are added in 64 bits). 8 x (8 + 8) x
+// 65536 rows of 64: 505 us with four waves, 497 so.
 struct BwdGrid {
   int n_q, blocks;
 };

@@ -107,9 +107,10 @@ def qk_norm_rope(q, k, q_weight, k_weight, *, eps=1e-6, rotate=True, rope_base=1
     q [L, B, Hq, T, D], k [L, B, Hkv, T, D]: bf16 or fp32 with contiguous rows,
     otherwise of any strides (views of a projection's output).  q_weight,
     k_weight: fp32 [L, D], or both None for the rotation alone.  Row t is at
-    position pos0 + t; rotate=False leaves the rotation to the attention (fwd()
-    and decode() rotate by themselves).  q_out may be a contiguous q, k_out a
-    contiguous k."""
+    position pos0 + t.  rotate=False leaves the rotation to the attention: with
+    fwd(), bwd() and decode(), which rotate by themselves, it has to be False, or
+    rows are rotated twice; the default is for attention over rotated rows.  q_out
+    may be a contiguous q, k_out a contiguous k."""
     return _calls().qk_norm_rope(stream, q, k, q_weight, k_weight, eps, rotate, rope_base, pos0,
                                  q_out, k_out)
 
@@ -117,8 +118,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, *, eps=1e-6, rotate=True, rope_base=1
 def qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, *, eps=1e-6, rotate=True,
                      rope_base=10000.0, pos0=0, dq=None, dk=None, dq_weight=None, dk_weight=None,
                      workspace=None, stream=None):
-    """Gradients of qk_norm_rope for its outputs' gradients dq_out, dk_out
-    (shaped like q and k, rows contiguous): returns contiguous (dq, dk) and the
+    """Gradients of qk_norm_rope, called with the same rotate, for its outputs'
+    gradients dq_out, dk_out (shaped like q and k, rows contiguous): returns contiguous (dq, dk) and the
     fp32 [L, D] gradients of the weights (None, None without weights), summed in a
     fixed order.  dq may be a contiguous dq_out, dk a contiguous dk_out.
     workspace: an optional CUDA uint8 buffer of qk_norm_workspace_size() bytes, for
@@ -147,7 +148,9 @@ def cache_append(q, k, v, cache, page_table, cu_q, cached, *, q_weight=None, k_w
     whose values do not matter and whose q_out stays as it was.  Row r of a sequence
     lies in slot r % page_size of page page_table[b, r // page_size].  cu_q [B + 1],
     cached [B] and page_table [B, max_pages] are int32 and read on the device.  No
-    two sequences with new tokens may share the pages that are written."""
+    two sequences with new tokens may share the pages that are written.  A table of
+    cosines for all max_pages * page_size positions (4 D bytes each) is kept on the
+    device."""
     return _calls().cache_append(stream, q, k, v, cache, page_table, cu_q, cached, q_weight,
                                  k_weight, eps, rope_base, q_out)
 
@@ -158,7 +161,9 @@ def cache_read(cache, page_table, lengths, *, rows=None, dtype=None, k_out=None,
     (k, v) [L, B, Hkv, rows, D] (sparse_attn_cache_read): the stored, rotated keys
     and the values; float8_e4m3fn pages are read as dtype (bf16 by default).
     rows defaults to all that the page table covers, or to k_out's (whose rows and
-    dtype any given rows= and dtype= have to be); rows from lengths[b] on are left as they were (zeros where the output is made here)."""
+    dtype any given rows= and dtype= have to be); rows from lengths[b] on are left
+    as they were (zeros where the output is made here, which is filled with them
+    first: a large read takes twice as long as into given outputs)."""
     return _calls().cache_read(stream, cache, page_table, lengths, rows, dtype, k_out, v_out)
 
 
