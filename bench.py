@@ -241,14 +241,14 @@ def decode_bytes_per_token_head(wl, elt):
 # capture per entry; keyed by workload, kernel and the hash of the kernel
 # sources the capture ran (kernel_source_hash): a changed source reports null.
 MEASURED_TRAFFIC = {
-    "learned_train/bwd_q_fast@cfbf3273cb54": 778.8,
-    "pi_gate_train/bwd_q_fast@cfbf3273cb54": 545.3,
-    "paper_fwd/fwd_fast@cfbf3273cb54": 494.1,
-    "extrap_4x/fwd_fast@cfbf3273cb54": 495.8,
-    "pow2_extrap/fwd_fast@cfbf3273cb54": 496.0,
-    "pi_skip/fwd_fast@cfbf3273cb54": 491.1,
-    "long_sinks/fwd_tc@cfbf3273cb54": 508.4,
-    "decode_4k/decode@cfbf3273cb54": 8120.2,
+    "learned_train/bwd_q_fast@e2818f3177aa": 780.3,
+    "pi_gate_train/bwd_q_fast@e2818f3177aa": 546.3,
+    "paper_fwd/fwd_fast@e2818f3177aa": 494.1,
+    "extrap_4x/fwd_fast@e2818f3177aa": 496.2,
+    "pow2_extrap/fwd_fast@e2818f3177aa": 495.9,
+    "pi_skip/fwd_fast@e2818f3177aa": 491.0,
+    "long_sinks/fwd_tc@e2818f3177aa": 509.1,
+    "decode_4k/decode@e2818f3177aa": 8121.5,
 }
 
 
